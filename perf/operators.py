@@ -11,7 +11,7 @@ import torch
 own = False
 
 _DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
-_WORKSPACE = 8 << 20      # bytes; the library's own query stays below this for every head layout drawn here
+_WORKSPACE = 16 << 20     # bytes; the library's own query stays below this for every head layout drawn here
 
 
 def listed():
