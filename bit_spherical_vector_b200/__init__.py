@@ -33,6 +33,18 @@ class svq_matrix(ctypes.Structure):
                 ("perm", ctypes.c_void_p), ("radius_lut", ctypes.c_void_p)]
 
 
+class svq_kv_cache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class svq_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -51,7 +63,7 @@ def lib():
         raise ImportError(f"libsvq.so not found at {LIB_PATH}; build it with "
                           "`python -m bit_spherical_vector_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
-    P, I, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    P, I, SZ, L64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
     MP = ctypes.POINTER(svq_matrix)
     sig = {
         "svq_status_string": ([I], ctypes.c_char_p),
@@ -75,6 +87,11 @@ def lib():
         "svq_moe_grouped_gemv": ([P, I, I, I, I, P, I, I, P, I, I, P, I, I, P, SZ, P], I),
         "svq_rmsnorm_permute": ([P, I, P, ctypes.c_float, I, I, ctypes.POINTER(P), ctypes.POINTER(P), I, P], I),
         "svq_swiglu_permute": ([P, P, I, I, P, P, P], I),
+        "svq_kv_assign": ([P, P, I, I, P, I, P, I, P, P, P, P, P, P, I, P], I),
+        "svq_rope_frequencies": ([I, ctypes.c_double, I, ctypes.c_double, I, P, P], I),
+        "svq_qk_norm_rope_cache": ([P, P, P, I, L64, L64, L64, I, I, P, P, ctypes.c_float, P, P, P, P, P, P], I),
+        "svq_paged_attention_workspace_size": ([P, I, ctypes.POINTER(SZ)], I),
+        "svq_paged_attention": ([P, I, I, P, P, P, I, P, I, ctypes.c_float, P, P, I, P, P, SZ, P], I),
         "svq_get_device_status": ([P], I),
         "svq_esg": ([P, I, I, ctypes.c_double, P, P, P, P], I),
         "svq_radius_grid": ([P, I, I, P, I, P, P, P], I),
@@ -336,6 +353,155 @@ def svq_swiglu_permute(gate, up, perm, x, stream=None):
     M, I = gate.shape
     _check(lib().svq_swiglu_permute(_ptr(gate), _ptr(up), M, I, _ptr(perm), _ptr(x), _stream(stream)),
            "svq_swiglu_permute")
+
+
+# ------------------------------------------------------------------ attention step (paged cache)
+SVQ_ROPE_PLAIN, SVQ_ROPE_LINEAR, SVQ_ROPE_NTK, SVQ_ROPE_YARN = range(4)
+
+
+def _need(ok: bool, what: str):
+    """Shapes, types and devices that the C ABI cannot see behind a pointer."""
+    if not ok:
+        raise ValueError(what)
+
+
+def _on_device(what: str, *tensors):
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{what}: tensors must be on the current CUDA device")
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _i32(what: str, *tensors):
+    import torch
+    for t in tensors:
+        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{what}: integer arrays must be contiguous int32")
+
+
+class KvCache:
+    """A paged key/value cache and its C descriptor: k and v are views [n_pages][page_size][n_heads][head_dim]
+    (fp16 or bf16) of the pools, in any order in memory with the head's entries contiguous."""
+
+    def __init__(self, k, v):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.stride() == v.stride(),
+              "KvCache: k and v must be alike, [n_pages][page_size][n_heads][head_dim]")
+        _need(k.stride(3) == 1, "KvCache: the entries of a head must be contiguous")
+        _need(k.get_device() == v.get_device(), "KvCache: k and v must be on one device")
+        self.k, self.v, self.dtype = k, v, k.dtype
+        self.n_pages, self.page_size, self.n_heads, self.head_dim = (int(d) for d in k.shape)
+        self.desc = svq_kv_cache(_dtype_code(k.dtype), self.n_pages, self.page_size, self.n_heads, self.head_dim, 0,
+                                 k.stride(0), k.stride(1), k.stride(2), k.data_ptr(), v.data_ptr())
+        self._ref = ctypes.addressof(self.desc)
+
+
+class Rope:
+    """Rotary positions and their C descriptor: inv_freq (fp64 [rot_dim / 2], radians per position, on the device),
+    the pair layout and the factor on rotated entries."""
+
+    def __init__(self, inv_freq, interleaved: bool = False, factor: float = 1.0):
+        import torch
+        _need(inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous() and inv_freq.is_cuda,
+              "Rope: inv_freq must be a contiguous fp64 vector on the device")
+        self.inv_freq, self.interleaved, self.factor = inv_freq, bool(interleaved), float(factor)
+        self.rot_dim = 2 * inv_freq.numel()
+        self.desc = svq_rope(inv_freq.data_ptr(), self.rot_dim, int(self.interleaved), self.factor, 0)
+        self._ref = ctypes.addressof(self.desc)
+
+    @classmethod
+    def make(cls, rot_dim: int, base: float, scaling: int = SVQ_ROPE_PLAIN, scale: float = 1.0, trained_len: int = 0,
+             interleaved: bool = False, device="cuda"):
+        """The frequencies of svq_rope_frequencies, on the device."""
+        import torch
+        freq, factor = svq_rope_frequencies(rot_dim, base, scaling, scale, trained_len)
+        return cls(torch.from_numpy(freq).to(device), interleaved, factor)
+
+
+def svq_rope_frequencies(rot_dim: int, base: float, scaling: int = SVQ_ROPE_PLAIN, scale: float = 1.0,
+                         trained_len: int = 0):
+    """Radians per position of each rotated pair (numpy fp64 [rot_dim / 2]) and the factor on rotated entries."""
+    import numpy as np
+    freq, factor = np.empty(max(rot_dim // 2, 1), np.float64), ctypes.c_float(0)
+    _check(lib().svq_rope_frequencies(rot_dim, float(base), scaling, float(scale), trained_len, freq.ctypes.data,
+                                      ctypes.addressof(factor)), "svq_rope_frequencies")
+    return freq, float(factor.value)
+
+
+def svq_kv_assign(lens, n_new, page_size: int, block_table, free_pages, n_free, lens_out, n_free_out, cu_rows,
+                  positions, slots, stream=None):
+    """Block table, positions and slots of one step from the requests' lengths: request b holds lens[b] tokens and
+    gets n_new[b] (negative: it is done).  All int32 on the device; lens_out may be lens, n_free_out may be n_free."""
+    what = "svq_kv_assign"
+    n, rows = lens.numel(), slots.numel()
+    _i32(what, lens, n_new, block_table, free_pages, n_free, lens_out, n_free_out, cu_rows, positions, slots)
+    _on_device(what, lens, n_new, block_table, free_pages, n_free, lens_out, n_free_out, cu_rows, positions, slots)
+    _need(block_table.dim() == 2 and block_table.shape[0] == n and n_new.numel() == n and lens_out.numel() == n
+          and cu_rows.numel() == n + 1 and positions.numel() == rows and n_free.numel() == 1
+          and n_free_out.numel() == 1, f"{what}: sizes do not agree")
+    _check(lib().svq_kv_assign(lens.data_ptr(), n_new.data_ptr(), n, page_size, block_table.data_ptr(),
+                               block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
+                               lens_out.data_ptr(), n_free_out.data_ptr(), cu_rows.data_ptr(), positions.data_ptr(),
+                               slots.data_ptr(), rows, _stream(stream)), what)
+
+
+def svq_qk_norm_rope_cache(q, k, v, q_gamma, k_gamma, eps: float, rope: Rope, positions, slots, cache: KvCache, q_out,
+                           stream=None):
+    """q [M][n_q * D], k and v [M][n_heads * D] (fp32, fp16 or bf16, rows any multiple of 8 apart) -> q_out
+    [M][n_q][D] and the cache's slots; gammas fp16 [D] or None; rows with a negative slot are left out."""
+    import torch
+    what = "svq_qk_norm_rope_cache"
+    M, D = q.shape[0], cache.head_dim
+    wq, wk = q_out.shape[1] * D, cache.n_heads * D
+    _need(q.shape == (M, wq) and k.shape == (M, wk) and v.shape == (M, wk) and q_out.shape[0] == M
+          and q_out.shape[2] == D and positions.numel() == M and slots.numel() == M, f"{what}: sizes do not agree")
+    _need(q.dtype == k.dtype == v.dtype and q_out.dtype == cache.dtype and q_out.is_contiguous()
+          and (M == 0 or q.stride(1) == k.stride(1) == v.stride(1) == 1), f"{what}: types or strides do not agree")
+    for g in (q_gamma, k_gamma):
+        _need(g is None or (g.dtype is torch.float16 and g.numel() == D and g.is_contiguous()),
+              f"{what}: gamma must be fp16 [head_dim]")
+    _i32(what, positions, slots)
+    _on_device(what, q, k, v, q_gamma, k_gamma, rope.inv_freq, positions, slots, cache.k, q_out)
+    ld = (q.stride(0), k.stride(0), v.stride(0)) if M > 1 else (wq, wk, wk)
+    _check(lib().svq_qk_norm_rope_cache(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q.dtype), *ld, M,
+                                        q_out.shape[1], _opt(q_gamma), _opt(k_gamma), eps, rope._ref,
+                                        positions.data_ptr(), slots.data_ptr(), cache._ref, q_out.data_ptr(),
+                                        _stream(stream)), what)
+
+
+def svq_paged_attention_workspace_size(cache: KvCache, n_q_heads: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().svq_paged_attention_workspace_size(cache._ref, n_q_heads, ctypes.byref(n)),
+           "svq_paged_attention_workspace_size")
+    return int(n.value)
+
+
+def svq_paged_attention(q, cache: KvCache, lens, block_table, scale: float, out, ws, cu_rows=None, order=None,
+                        lse=None, stream=None):
+    """out [rows][n_q * D] (fp16 or bf16) = attention of q [rows][n_q][D] over the first lens[b] tokens of request b
+    (row b, or row cu_rows[b + 1] - 1).  order (int32 [n_q * D]): column of each entry, the inverse of the o
+    matrix's perm for its stored order; lse: fp32 [rows][n_q] or None.  ws: zero-filled once by svq_workspace_init."""
+    import torch
+    what = "svq_paged_attention"
+    rows, heads, D = q.shape
+    n = lens.numel()
+    _need(D == cache.head_dim and out.shape == (rows, heads * D) and block_table.dim() == 2
+          and block_table.shape[0] == n and (cu_rows.numel() == n + 1 if cu_rows is not None else n <= rows)
+          and (order is None or order.numel() == heads * D)
+          and (lse is None or (lse.shape == (rows, heads) and lse.dtype is torch.float32 and lse.is_contiguous())),
+          f"{what}: sizes do not agree")
+    _need(q.dtype == cache.dtype and q.is_contiguous() and out.is_contiguous() and ws.is_contiguous(),
+          f"{what}: types or strides do not agree")
+    _i32(what, lens, block_table, cu_rows, order)
+    _on_device(what, q, cache.k, lens, block_table, out, ws, cu_rows, order, lse)
+    _check(lib().svq_paged_attention(q.data_ptr(), rows, heads, cache._ref, lens.data_ptr(), _opt(cu_rows), n,
+                                     block_table.data_ptr(), block_table.shape[1], scale, _opt(order),
+                                     out.data_ptr(), _dtype_code(out.dtype), _opt(lse), ws.data_ptr(),
+                                     ws.numel() * ws.element_size(), _stream(stream)), what)
 
 
 # ------------------------------------------------------------------ calibration (ESG, radius grid, encoder, ABS)

@@ -5,9 +5,11 @@
 
 #include <mutex>
 
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
+#include "attn_params.h"
 #include "layout.cuh"
 #include "svq.h"
 #include "gemm_params.h"
@@ -148,6 +150,29 @@ int* status_word() {
     ptr[dev] = static_cast<int*>(p);
   }
   return ptr[dev];
+}
+
+// A paged cache as the kernels take it: heads of 64, 128 or 256 entries, whole
+// 16-byte chunks everywhere, and a slot number (page * page_size + token) that
+// fits 32 bits.
+int check_cache(const svq_kv_cache* c) {
+  if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return SVQ_ERR_INVALID_ARG;
+  if (c->dtype != SVQ_F16 && c->dtype != SVQ_BF16) return SVQ_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->page_size < 1 || c->n_heads < 1 || c->reserved != 0) return SVQ_ERR_INVALID_ARG;
+  if (c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0 || c->page_stride % 8 || c->token_stride % 8 ||
+      c->head_stride % 8)
+    return SVQ_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return SVQ_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)c->n_pages * c->page_size > INT32_MAX || c->n_heads > 1024) return SVQ_ERR_UNSUPPORTED_SHAPE;
+  return SVQ_OK;
+}
+
+svq::KvView view_of(const svq_kv_cache& c) {
+  svq::KvView v;
+  v.k = static_cast<uint16_t*>(c.k); v.v = static_cast<uint16_t*>(c.v);
+  v.page_stride = c.page_stride; v.token_stride = c.token_stride; v.head_stride = c.head_stride;
+  v.n_pages = c.n_pages; v.page_size = c.page_size; v.n_heads = c.n_heads;
+  return v;
 }
 
 }  // namespace
@@ -410,6 +435,149 @@ int svq_swiglu_permute(const float* gate, const float* up, int M, int I, const i
   if (!gate || !up || !x || !aligned(gate, 16) || !aligned(up, 16) || !aligned(x, 16)) return SVQ_ERR_INVALID_ARG;
   if (perm && !aligned(perm, 4)) return SVQ_ERR_INVALID_ARG;
   return cuda_status(svq::launch_swiglu_permute(gate, up, M, I, perm, x, (cudaStream_t)stream));
+}
+
+int svq_rope_frequencies(int rot_dim, double base, int scaling, double scale, int trained_len, double* inv_freq,
+                         float* factor) {
+  if (!inv_freq || !factor) return SVQ_ERR_INVALID_ARG;
+  if (rot_dim < 16 || rot_dim > 256 || rot_dim % 16 != 0) return SVQ_ERR_UNSUPPORTED_SHAPE;
+  if (!(base > 1.0) || base > 1e300) return SVQ_ERR_INVALID_ARG;
+  if (scaling < SVQ_ROPE_PLAIN || scaling > SVQ_ROPE_YARN) return SVQ_ERR_INVALID_ARG;
+  if (scaling != SVQ_ROPE_PLAIN && (!(scale >= 1.0) || scale > 1e6)) return SVQ_ERR_INVALID_ARG;
+  if (scaling == SVQ_ROPE_YARN && trained_len < 1) return SVQ_ERR_INVALID_ARG;
+  const int half = rot_dim / 2;
+  *factor = 1.0f;
+  if (scaling == SVQ_ROPE_NTK) base *= std::pow(scale, (double)rot_dim / (rot_dim - 2));
+  for (int i = 0; i < half; ++i) inv_freq[i] = std::pow(base, -2.0 * i / rot_dim);
+  if (scaling == SVQ_ROPE_LINEAR)
+    for (int i = 0; i < half; ++i) inv_freq[i] /= scale;
+  if (scaling == SVQ_ROPE_YARN) {
+    // pair index whose frequency makes the given number of turns over the trained length
+    const double two_pi = 6.283185307179586476925;
+    const auto at = [&](double turns) {
+      return rot_dim * std::log(trained_len / (turns * two_pi)) / (2.0 * std::log(base));
+    };
+    const double lo = std::fmax(std::floor(at(32.0)), 0.0), hi = std::fmin(std::ceil(at(1.0)), rot_dim - 1.0);
+    for (int i = 0; i < half; ++i) {
+      const double ramp = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      inv_freq[i] = inv_freq[i] / scale * ramp + inv_freq[i] * (1.0 - ramp);
+    }
+    *factor = (float)(0.1 * std::log(scale) + 1.0);
+  }
+  return SVQ_OK;
+}
+
+int svq_kv_assign(const int32_t* lens, const int32_t* n_new, int n_seqs, int page_size, int32_t* block_table,
+                  int max_pages, int32_t* free_pages, int n_pages, const int32_t* n_free, int32_t* lens_out,
+                  int32_t* n_free_out, int32_t* cu_rows, int32_t* positions, int32_t* slots, int max_rows,
+                  svq_stream_t stream) {
+  if (n_seqs < 1 || page_size < 1 || max_pages < 1 || n_pages < 1 || max_rows < 0) return SVQ_ERR_INVALID_ARG;
+  if (n_seqs > svq::kMaxSeqs || (int64_t)n_seqs * max_pages > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX ||
+      (int64_t)n_pages * page_size > INT32_MAX || max_rows > (1 << 30))
+    return SVQ_ERR_UNSUPPORTED_SHAPE;
+  const void* ptrs[] = {lens, n_new, block_table, free_pages, n_free, lens_out, n_free_out, cu_rows};
+  for (const void* q : ptrs)
+    if (!q || !aligned(q, 4)) return SVQ_ERR_INVALID_ARG;
+  if (max_rows > 0 && (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 4)))
+    return SVQ_ERR_INVALID_ARG;
+  int* status = status_word();
+  if (!status) return SVQ_ERR_CUDA;
+  svq::KvAssignParams p;
+  p.lens = lens; p.n_new = n_new; p.table = block_table; p.free_pages = free_pages; p.n_free = n_free;
+  p.lens_out = lens_out; p.n_free_out = n_free_out; p.cu_rows = cu_rows; p.positions = positions; p.slots = slots;
+  p.status = status;
+  p.n_seqs = n_seqs; p.width = max_pages; p.page_size = page_size; p.n_pages = n_pages; p.max_rows = max_rows;
+  return cuda_status(svq::launch_kv_assign(p, (cudaStream_t)stream));
+}
+
+int svq_qk_norm_rope_cache(const void* q, const void* k, const void* v, int x_dtype, int64_t ldq, int64_t ldk,
+                           int64_t ldv, int M, int n_q_heads, const uint16_t* q_gamma, const uint16_t* k_gamma,
+                           float eps, const svq_rope* rope, const int32_t* positions, const int32_t* slots,
+                           const svq_kv_cache* cache, uint16_t* q_out, svq_stream_t stream) {
+  const int st = check_cache(cache);
+  if (st != SVQ_OK) return st;
+  if (x_dtype != SVQ_F32 && x_dtype != SVQ_F16 && x_dtype != SVQ_BF16) return SVQ_ERR_INVALID_ARG;
+  if (!rope || !rope->inv_freq || !aligned(rope->inv_freq, 8) || rope->reserved != 0) return SVQ_ERR_INVALID_ARG;
+  if (rope->interleaved != 0 && rope->interleaved != 1) return SVQ_ERR_INVALID_ARG;
+  if (!(rope->factor >= -3.0e38f && rope->factor <= 3.0e38f)) return SVQ_ERR_INVALID_ARG;
+  if (rope->rot_dim < 16 || rope->rot_dim > cache->head_dim || rope->rot_dim % 16 != 0)
+    return SVQ_ERR_UNSUPPORTED_SHAPE;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return SVQ_ERR_INVALID_ARG;
+  if (M < 0 || M > (1 << 20) || n_q_heads < 1 || n_q_heads > 1024) return SVQ_ERR_INVALID_ARG;
+  if (M == 0) return SVQ_OK;                     // nothing to read or write
+  const int64_t q_row = (int64_t)n_q_heads * cache->head_dim, kv_row = (int64_t)cache->n_heads * cache->head_dim;
+  if (ldq < q_row || ldk < kv_row || ldv < kv_row || ldq % 8 || ldk % 8 || ldv % 8) return SVQ_ERR_INVALID_ARG;
+  if (!q || !k || !v || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !q_out || !aligned(q_out, 16))
+    return SVQ_ERR_INVALID_ARG;
+  if ((q_gamma && !aligned(q_gamma, 16)) || (k_gamma && !aligned(k_gamma, 16))) return SVQ_ERR_INVALID_ARG;
+  if (!positions || !slots || !aligned(positions, 4) || !aligned(slots, 4)) return SVQ_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  int* status = status_word();
+  if (sms <= 0 || !status) return SVQ_ERR_CUDA;
+  svq::RopeCacheParams p;
+  p.q = q; p.k = k; p.v = v; p.ldq = ldq; p.ldk = ldk; p.ldv = ldv;
+  p.q_gamma = q_gamma; p.k_gamma = k_gamma; p.inv_freq = rope->inv_freq; p.positions = positions; p.slots = slots;
+  p.q_out = q_out; p.status = status; p.kv = view_of(*cache); p.eps = eps; p.factor = rope->factor;
+  p.M = M; p.n_q = n_q_heads; p.rot = rope->rot_dim; p.interleaved = rope->interleaved;
+  return cuda_status(svq::launch_rope_cache(p, cache->head_dim, x_dtype == SVQ_F32 ? 0 : x_dtype == SVQ_F16 ? 1 : 2,
+                                            cache->dtype == SVQ_BF16, sms, (cudaStream_t)stream));
+}
+
+int svq_paged_attention_workspace_size(const svq_kv_cache* cache, int n_q_heads, size_t* bytes) {
+  if (!bytes) return SVQ_ERR_INVALID_ARG;
+  const int st = check_cache(cache);
+  if (st != SVQ_OK) return st;
+  const int sms = num_sms();
+  if (sms <= 0) return SVQ_ERR_CUDA;
+  svq::PagedAttnPlan plan;
+  if (!svq::plan_paged_attn(n_q_heads, cache->n_heads, cache->head_dim, 1, sms, &plan))
+    return SVQ_ERR_UNSUPPORTED_SHAPE;
+  *bytes = plan.ws_total;
+  return SVQ_OK;
+}
+
+int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_kv_cache* cache, const int32_t* lens,
+                        const int32_t* cu_rows, int n_seqs, const int32_t* block_table, int max_pages, float scale,
+                        const int32_t* order, void* out, int out_dtype, float* lse, void* workspace,
+                        size_t workspace_bytes, svq_stream_t stream) {
+  const int st = check_cache(cache);
+  if (st != SVQ_OK) return st;
+  if (out_dtype != SVQ_F16 && out_dtype != SVQ_BF16) return SVQ_ERR_INVALID_ARG;
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return SVQ_ERR_INVALID_ARG;      // rejects NaN and infinities
+  if (n_seqs < 0 || n_rows < 0 || max_pages < 1) return SVQ_ERR_INVALID_ARG;
+  // the tiles of all requests are counted in 32 bits
+  if (n_seqs > svq::kMaxSeqs || n_rows > (1 << 26) || (int64_t)max_pages * cache->page_size > INT32_MAX ||
+      n_seqs * ((int64_t)max_pages * cache->page_size / 16 + 1) > INT32_MAX || n_q_heads > 1024)
+    return SVQ_ERR_UNSUPPORTED_SHAPE;
+  svq::PagedAttnPlan plan;
+  const int sms = num_sms();
+  if (n_q_heads < 1 || n_q_heads % cache->n_heads != 0) return SVQ_ERR_UNSUPPORTED_SHAPE;
+  if (n_seqs == 0 || n_rows == 0) return SVQ_OK; // nothing to read or write
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !lens || !aligned(lens, 4) || !block_table ||
+      !aligned(block_table, 4))
+    return SVQ_ERR_INVALID_ARG;
+  if ((cu_rows && !aligned(cu_rows, 4)) || (order && !aligned(order, 4)) || (lse && !aligned(lse, 4)))
+    return SVQ_ERR_INVALID_ARG;
+  if (sms <= 0) return SVQ_ERR_CUDA;
+  if (!svq::plan_paged_attn(n_q_heads, cache->n_heads, cache->head_dim, n_seqs, sms, &plan))
+    return SVQ_ERR_UNSUPPORTED_SHAPE;
+  if (!workspace || workspace_bytes < plan.ws_total || !aligned(workspace, 256)) return SVQ_ERR_WORKSPACE;
+  int* status = status_word();
+  if (!status) return SVQ_ERR_CUDA;
+  char* w = static_cast<char*>(workspace);
+  svq::PagedAttnParams p;
+  p.q = q; p.lens = lens; p.cu_rows = cu_rows; p.table = block_table; p.order = order;
+  p.out = static_cast<uint16_t*>(out); p.lse = lse; p.status = status;
+  p.counters = reinterpret_cast<unsigned*>(w);
+  p.cta_part = reinterpret_cast<float*>(w + plan.cta_part);
+  p.warp_part = reinterpret_cast<float*>(w + plan.warp_part);
+  p.kv = view_of(*cache);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.n_seqs = n_seqs; p.width = max_pages; p.n_q = n_q_heads; p.n_rows = n_rows;
+  p.group = n_q_heads / cache->n_heads;
+  p.row_tiles = (p.group + plan.rows - 1) / plan.rows;
+  p.out_bf16 = out_dtype == SVQ_BF16;
+  return cuda_status(svq::launch_paged_attn(p, plan, cache->head_dim, cache->dtype == SVQ_BF16, (cudaStream_t)stream));
 }
 
 int svq_esg(const float* x_cal, int T, int K, double gamma, double* energy, int32_t* perm, float* weights,

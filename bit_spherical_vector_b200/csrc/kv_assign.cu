@@ -1,0 +1,207 @@
+// kv_assign.cu -- block tables and slot maps of one step, built on the GPU from
+// the requests' lengths.
+//
+// With ps tokens to a page, held_b = ceil(len_b / ps) pages of request b are in
+// its table row.  n_b >= 0 new tokens take need_b = ceil((len_b + n_b) / ps) -
+// held_b pages; n_b < 0 says that the request is done and releases its held_b.
+// The free pages are a stack: the n_free entries of the list, then the released
+// pages in request order; the k-th page that the step needs (request order) is
+// entry top - 1 - k.  Row r of the step belongs to the request with
+// cu[b] <= r < cu[b + 1], stands at position len_b + r - cu[b] and is kept in
+// slot page * ps + position % ps.
+//
+// The work is three prefix sums over the requests and a few words per row, so
+// latency bounds it: every CTA computes the prefix sums for itself (two loads
+// and one block scan), then the rows, the new table entries and the free list
+// are spread over all threads, each entry found by a binary search in shared
+// memory; no CTA reads what another writes.  The CTAs of a call form one
+// cluster and meet at its barrier once all of them have read the lengths and
+// the free count, so those two may be updated in place (a captured decode step
+// replayed again and again).
+#include "attn_params.h"
+#include "svq.h"
+
+namespace svq {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+
+// Last i in [0, n) with a[i] <= v, for nondecreasing a with a[0] <= v.
+__device__ __forceinline__ int find_segment(const int* a, int n, int v) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= v) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+struct Stack {                           // the step's free pages, bottom to top
+  const KvAssignParams& p;
+  const int* gone;                       // [n_seqs + 1] released pages before request b
+  int n_free;
+  __device__ int released(int i) const {
+    const int b = find_segment(gone, p.n_seqs, i);
+    return p.table[(size_t)b * p.width + (i - gone[b])];
+  }
+  __device__ int at(int i) const { return i < n_free ? p.free_pages[i] : released(i - n_free); }
+};
+
+__global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_constant__ KvAssignParams p) {
+  extern __shared__ int sm[];
+  const int n = p.n_seqs, ps = p.page_size;
+  int* len = sm;                         // [n]
+  int* cu = len + n;                     // [n + 1] rows before request b
+  int* need = cu + n + 1;                // [n + 1] pages needed before request b
+  int* gone = need + n + 1;              // [n + 1] pages released before request b
+  __shared__ long long w_rows[kWarps];
+  __shared__ int w_need[kWarps], w_gone[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x, ctas = gridDim.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // Each thread takes a run of consecutive requests.  Row counts are summed in
+  // 64 bits: a nonsense count must not wrap into a plausible total.  The page
+  // sums stay below 2^31 whenever the call is not refused (the host checks
+  // n_seqs * width, and need <= rows + n).
+  const int n_free = *p.n_free;
+  const long long room = (long long)p.width * ps;
+  const int per = (n + kThreads - 1) / kThreads;
+  const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
+  long long rows_t = 0;
+  int need_t = 0, gone_t = 0;
+  bool bad = n_free < 0 || n_free > p.n_pages;
+  for (int b = b0; b < b1; ++b) {
+    const int l = p.lens[b], a = p.n_new[b];
+    const long long to = (long long)l + max(a, 0);
+    bad |= l < 0 || to > room;
+    const int held = (int)(((long long)l + ps - 1) / ps);
+    len[b] = l;
+    cu[b] = a;                           // the new count for now
+    rows_t += max(a, 0);
+    need_t += a < 0 ? 0 : (int)((to + ps - 1) / ps) - held;
+    gone_t += a < 0 ? held : 0;
+  }
+  long long rows_i = rows_t;
+  int need_i = need_t, gone_i = gone_t;  // inclusive over the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long r = __shfl_up_sync(0xFFFFFFFFu, rows_i, o);
+    const int s = __shfl_up_sync(0xFFFFFFFFu, need_i, o), t = __shfl_up_sync(0xFFFFFFFFu, gone_i, o);
+    if (lane >= o) {
+      rows_i += r;
+      need_i += s;
+      gone_i += t;
+    }
+  }
+  if (lane == 31) {
+    w_rows[warp] = rows_i;
+    w_need[warp] = need_i;
+    w_gone[warp] = gone_i;
+  }
+  bad = __syncthreads_or(bad);
+  long long rows = rows_i - rows_t, rows_all = 0;
+  int need_b = need_i - need_t, gone_b = gone_i - gone_t, need_all = 0, gone_all = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      rows += w_rows[w];
+      need_b += w_need[w];
+      gone_b += w_gone[w];
+    }
+    rows_all += w_rows[w];
+    need_all += w_need[w];
+    gone_all += w_gone[w];
+  }
+  const long long top = (long long)n_free + gone_all;
+  const bool refuse = bad || rows_all > p.max_rows || need_all > top || top > p.n_pages;
+  for (int b = b0; b < b1; ++b) {
+    const int l = len[b], a = cu[b];
+    const int held = (int)(((long long)l + ps - 1) / ps);
+    cu[b] = (int)rows;
+    need[b] = need_b;
+    gone[b] = gone_b;
+    rows += max(a, 0);
+    need_b += a < 0 ? 0 : (int)(((long long)l + a + ps - 1) / ps) - held;
+    gone_b += a < 0 ? held : 0;
+    if (rank == 0) p.cu_rows[b] = refuse ? 0 : cu[b];
+  }
+  if (tid == 0) {
+    cu[n] = (int)rows_all;
+    need[n] = need_all;
+    gone[n] = gone_all;
+    if (rank == 0) p.cu_rows[n] = refuse ? 0 : (int)rows_all;
+  }
+  // All CTAs have read the lengths and the free count (also the barrier that
+  // publishes the prefix sums inside each CTA).
+  if (ctas > 1) {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
+  }
+  if (rank == 0) {
+    for (int b = b0; b < b1; ++b) {
+      const int l = len[b];
+      int to = l;
+      if (!refuse) {
+        // done requests are the ones with pages released or an empty row and a
+        // negative count; the count itself is still in p.n_new
+        const int a = p.n_new[b];
+        to = a < 0 ? 0 : l + a;
+      }
+      p.lens_out[b] = to;
+    }
+    if (tid == 0) {
+      *p.n_free_out = refuse ? n_free : (int)(top - need_all);
+      if (refuse) *p.status = SVQ_ERR_INVALID_ARG;
+    }
+  }
+  const int g = rank * kThreads + tid, gn = ctas * kThreads;
+  if (refuse) {
+    for (int r = g; r < p.max_rows; r += gn) {
+      p.positions[r] = -1;
+      p.slots[r] = -1;
+    }
+    return;
+  }
+  const Stack stack{p, gone, n_free};
+  const int itop = (int)top;
+  for (int r = g; r < p.max_rows; r += gn) {
+    int pos = -1, slot = -1;
+    if (r < (int)rows_all) {
+      const int b = find_segment(cu, n, r);
+      const int l = len[b];
+      pos = l + (r - cu[b]);
+      const int held = (int)(((long long)l + ps - 1) / ps), j = pos / ps;
+      const int page = j < held ? p.table[(size_t)b * p.width + j] : stack.at(itop - 1 - (need[b] + j - held));
+      if ((unsigned)page < (unsigned)p.n_pages) slot = page * ps + (pos - j * ps);
+      else *p.status = SVQ_ERR_INVALID_ARG;
+    }
+    p.positions[r] = pos;
+    p.slots[r] = slot;
+  }
+  for (int k = g; k < need_all; k += gn) {
+    const int b = find_segment(need, n, k);
+    const int held = (int)(((long long)len[b] + ps - 1) / ps);
+    p.table[(size_t)b * p.width + held + (k - need[b])] = stack.at(itop - 1 - k);
+  }
+  // released pages that the step does not take go onto the list
+  for (int i = n_free + g; i < itop - need_all; i += gn) p.free_pages[i] = stack.released(i - n_free);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_assign(const KvAssignParams& p, cudaStream_t st) {
+  const size_t smem = (size_t)(4 * p.n_seqs + 3) * sizeof(int);
+  const unsigned ctas = p.max_rows > 4096 ? 8 : 1;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kv_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(kv_assign_kernel, ctas, kThreads, smem, ctas, st, p);
+}
+
+}  // namespace svq

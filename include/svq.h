@@ -345,6 +345,156 @@ SVQ_API int svq_swiglu_permute(const float* gate, const float* up, int M, int I,
                                svq_stream_t stream);
 
 /*
+ * The attention step of a decoder layer, between its q|k|v and o linears, over a
+ * paged key/value cache.  The pages evaluate SVQ inside Qwen3 models (abstract)
+ * without describing their attention; the formulas are stated with each call.
+ * All calls are launched as programmatic dependents like the GEMV, read their
+ * inputs only after the previous kernel on `stream` has completed (gammas and
+ * inv_freq may be read earlier: they are weights), and write results that do
+ * not depend on timing.
+ *
+ * svq_kv_cache -- a pool of pages for keys and one for values: entry d of key
+ * head h of the token at place t of a page is element
+ *   page * page_stride + t * token_stride + h * head_stride + d
+ * of k (and of v), so [page][token][head][d], [page][head][token][d] and pools
+ * that interleave k and v are all described.  Strides in elements, multiples of
+ * 8; k and v 16-byte aligned; dtype SVQ_F16 or SVQ_BF16; head_dim 64, 128 or 256;
+ * n_pages * page_size < 2^31.  Any page_size >= 1.  A token's slot is
+ * page * page_size + t.
+ */
+typedef struct svq_kv_cache {
+  int32_t dtype;          /* SVQ_F16 or SVQ_BF16                     */
+  int32_t n_pages;
+  int32_t page_size;      /* tokens per page                         */
+  int32_t n_heads;        /* key/value heads (at most 1024)          */
+  int32_t head_dim;       /* 64, 128 or 256                          */
+  int32_t reserved;       /* must be 0                               */
+  int64_t page_stride, token_stride, head_stride; /* elements        */
+  void* k;
+  void* v;
+} svq_kv_cache;
+
+/*
+ * svq_kv_assign -- block tables and slot maps of one step, built on the GPU.
+ * Request b (b < n_seqs <= 4096) holds lens[b] tokens in the first
+ * ceil(lens[b] / page_size) pages of its row of block_table ([n_seqs][max_pages]
+ * int32).  n_new[b] >= 0 new tokens are added; n_new[b] < 0 says that the request
+ * is done and its pages are free again.  The free pages are a stack, free_pages
+ * [n_pages] with *n_free entries; the step's stack is those, then the pages of
+ * done requests in request order, and pages are taken from its top in request
+ * order (the k-th page needed is entry top - 1 - k).  Written:
+ *   cu_rows [n_seqs + 1]   rows of the step before each request (sum of n_new >= 0)
+ *   positions [max_rows]   lens[b] + r - cu_rows[b] for row r of request b
+ *   slots [max_rows]       its slot; rows from cu_rows[n_seqs] on: -1, -1
+ *   block_table            the new pages behind the old ones (other entries: untouched)
+ *   free_pages             released pages that the step did not take, from entry *n_free on
+ *   lens_out [n_seqs]      lens + n_new, 0 for a done request; may be lens itself
+ *   n_free_out [1]         entries of the stack after the step; may be n_free itself
+ * With lens_out and n_free_out in buffers of their own the call can be repeated
+ * with the same effect.  All or nothing: when a length is negative or does not
+ * fit max_pages, the rows exceed max_rows, the pages do not suffice or *n_free
+ * lies outside 0..n_pages, then lens_out = lens, *n_free_out = *n_free, cu_rows
+ * = 0 and all rows -1, nothing else is written, and the device status word is set to
+ * SVQ_ERR_INVALID_ARG.  A page number outside 0..n_pages-1 in the table or the
+ * list gives slot -1 and sets the status word.  n_pages * page_size, max_pages *
+ * page_size and n_seqs * max_pages < 2^31, max_rows <= 2^30.
+ */
+SVQ_API int svq_kv_assign(const int32_t* lens, const int32_t* n_new, int n_seqs, int page_size,
+                          int32_t* block_table, int max_pages, int32_t* free_pages, int n_pages,
+                          const int32_t* n_free, int32_t* lens_out, int32_t* n_free_out, int32_t* cu_rows,
+                          int32_t* positions, int32_t* slots, int max_rows, svq_stream_t stream);
+
+/*
+ * svq_rope -- rotary positions: inv_freq [rot_dim / 2] (device, fp64, radians per
+ * position) for the pairs (i, i + rot_dim / 2) (interleaved 0) or (2i, 2i + 1)
+ * (interleaved 1) of the first rot_dim entries of each head (a multiple of 16, at
+ * most head_dim); the rest of the head is not rotated.  factor multiplies the
+ * rotated entries (1 unless the context is stretched).
+ *
+ * svq_rope_frequencies -- a HOST computation: fills host arrays inv_freq
+ * [rot_dim / 2] and factor[1] for theta_i = base^(-2i / rot_dim) and
+ *   SVQ_ROPE_PLAIN   theta_i
+ *   SVQ_ROPE_LINEAR  theta_i / scale                     (position interpolation)
+ *   SVQ_ROPE_NTK     theta_i with base * scale^(rot_dim / (rot_dim - 2))
+ *   SVQ_ROPE_YARN    theta_i below 1 turn over trained_len divided by scale, above
+ *                    32 turns unchanged, a linear ramp over the pair index between,
+ *                    and factor = 0.1 ln(scale) + 1 (YaRN, arXiv 2309.00071)
+ * base > 1, scale >= 1 (ignored by SVQ_ROPE_PLAIN), trained_len >= 1 (SVQ_ROPE_YARN).
+ */
+typedef struct svq_rope {
+  const double* inv_freq; /* device, 8-byte aligned */
+  int32_t rot_dim;
+  int32_t interleaved;
+  float factor;
+  int32_t reserved;       /* must be 0 */
+} svq_rope;
+
+enum svq_rope_scaling { SVQ_ROPE_PLAIN = 0, SVQ_ROPE_LINEAR = 1, SVQ_ROPE_NTK = 2, SVQ_ROPE_YARN = 3 };
+
+SVQ_API int svq_rope_frequencies(int rot_dim, double base, int scaling, double scale, int trained_len,
+                                 double* inv_freq /* host */, float* factor /* host */);
+
+/*
+ * svq_qk_norm_rope_cache -- from the outputs of q|k|v to the attention's inputs,
+ * for rows m < M and every head of head_dim entries:
+ *   n = x * gamma / sqrt(mean(x^2) + eps)       (q and k; gamma NULL: n = x)
+ *   (u, w) -> factor * (u cos a - w sin a, u sin a + w cos a),  a = positions[m] * inv_freq[i]
+ * rounded once to the cache's type.  Rotated queries go to q_out
+ * [M][n_q_heads][head_dim], keys and (unchanged) values to their slot slots[m].
+ * Rows with a negative slot are padding: nothing of them is read or written.  A
+ * slot beyond the cache is skipped and sets the device status word.  The rows'
+ * slots must be distinct (of two rows with one slot either may win, entry by entry).
+ * q [M][n_q_heads * head_dim], k and v [M][n_heads * head_dim] of x_dtype (SVQ_F32,
+ * SVQ_F16 or SVQ_BF16), 16-byte aligned, rows ldq, ldk, ldv elements apart
+ * (multiples of 8; three views of one fused output are fine); gammas fp16
+ * [head_dim], 16-byte aligned; q_out 16-byte aligned.  The angle is reduced in
+ * fp64: its error is below 1e-6 at any position below 10^8.  0 <= M <= 2^20,
+ * n_q_heads <= 1024.  Tolerance used by the tests: half a step of the output type
+ * plus 8e-6 of the pair's magnitude.
+ */
+SVQ_API int svq_qk_norm_rope_cache(const void* q, const void* k, const void* v, int x_dtype, int64_t ldq,
+                                   int64_t ldk, int64_t ldv, int M, int n_q_heads, const uint16_t* q_gamma,
+                                   const uint16_t* k_gamma, float eps, const svq_rope* rope /* host struct */,
+                                   const int32_t* positions, const int32_t* slots,
+                                   const svq_kv_cache* cache /* host struct */, uint16_t* q_out, svq_stream_t stream);
+
+/*
+ * svq_paged_attention -- attention of one token per request over the cache: with
+ * the first lens[b] tokens of request b's pages, for each query head h and its key
+ * head h / (n_q_heads / n_heads),
+ *   s_j = scale * q . k_j,  p = softmax(s),  o = sum_j p_j v_j
+ * (scores and sums fp32, the softmax weights carried in two terms of the cache's
+ * type, o rounded once).  n_q_heads a multiple of n_heads, at most 1024.
+ * Rows: with cu_rows NULL request b is row b of q, out and lse; with cu_rows
+ * [n_seqs + 1] (svq_kv_assign's) it is row cu_rows[b + 1] - 1, its last row of the
+ * step, and a request without a row is left out.  Other rows of out and lse are
+ * left as they are.  A request of length 0 gives zeros and lse -inf.  Entries of
+ * the cache and the table behind a request's length are not looked at.
+ * q: [n_rows][n_q_heads][head_dim] of the cache's type.  out: [n_rows][n_q_heads *
+ * head_dim] of out_dtype SVQ_F16 or SVQ_BF16, entry s = h * head_dim + d at column
+ * order[s] (device int32 [n_q_heads * head_dim]; NULL: s).  With order the inverse of
+ * o's perm (order[perm[j]] = j) the row is o's input in its stored column order,
+ * for a descriptor with perm NULL.  lse: fp32 [n_rows][n_q_heads] natural
+ * logarithm of the sum of e^s, or NULL.
+ * Lengths, rows, page numbers and order are checked on the device: a length
+ * outside 0..max_pages * page_size is clamped, a row outside 0..n_rows-1 is left
+ * out, a key on a page outside the pool does not count, an entry of order outside
+ * the row is not written; each sets the device status word to SVQ_ERR_INVALID_ARG.
+ * n_seqs <= 4096 and n_seqs * (max_pages * page_size / 16 + 1) < 2^31.
+ * Workspace (svq_paged_attention_workspace_size; the lengths and n_seqs do not
+ * matter): completion counters in its first 64 KiB, zero before the first call
+ * (svq_workspace_init), left zero by every completed call, then parts of split
+ * requests.  One workspace can serve svq_linear_gemv calls and these in turn;
+ * calls that share one must not overlap on the GPU.
+ */
+SVQ_API int svq_paged_attention_workspace_size(const svq_kv_cache* cache /* host struct */, int n_q_heads,
+                                               size_t* bytes);
+SVQ_API int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_kv_cache* cache /* host struct */,
+                                const int32_t* lens, const int32_t* cu_rows, int n_seqs, const int32_t* block_table,
+                                int max_pages, float scale, const int32_t* order, void* out, int out_dtype, float* lse,
+                                void* workspace, size_t workspace_bytes, svq_stream_t stream);
+
+/*
  * Calibration side (offline, before svq_repack): Energy-Stratified Grouping,
  * the per-row radius grid, the activation-weighted encoder and Adaptive Bit
  * Split ("SAGE", abstract; Figure 2 caption: signs, direction index and

@@ -1,0 +1,167 @@
+"""Host logic of decode attention's split (no GPU): the kernel's own range and cursor functions, compiled into
+a host program and walked the way the kernel walks them.
+
+For seeded batches (one to 600 requests, lengths 0 to thousands, 1 to 64 heads and row tiles, 4 and 8 warps,
+148 CTAs and fewer) every tile of every unit must be visited exactly once, in order; every unit must be
+written exactly once: by the one warp that has all of it, by the one CTA that has all of it, or by the last
+of the CTAs from range_of(first tile) to range_of(last tile), which are exactly the CTAs that leave a part of
+it; no CTA uses a workspace slot twice, no warp a part slot twice, and a counter (that of the unit's first CTA)
+belongs to one unit and gets as many arrivals as the unit has CTAs.  Places beyond 2^31 are checked on the range
+functions alone."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from bit_spherical_vector_b200 import build as svq_build
+
+HARNESS = r"""
+#include <cstdio>
+#include <map>
+#include <random>
+#include <set>
+#include <vector>
+#include "attn_split.cuh"
+using namespace svq;
+static long long bad = 0, cases = 0, split_units = 0;
+#define CHECK(c, ...) do { if (!(c)) { if (++bad < 20) { printf(__VA_ARGS__); printf("\n"); } } } while (0)
+
+static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
+  const int n = (int)lens.size();
+  std::vector<int> pre(n + 1, 0);
+  std::vector<uint32_t> meta(n);
+  for (int b = 0; b < n; ++b) {
+    const int nt = (lens[b] + kAttnTile - 1) / kAttnTile;
+    pre[b + 1] = pre[b] + nt;
+    meta[b] = ((uint32_t)b << 4) | (uint32_t)(nt * kAttnTile - lens[b]);
+  }
+  const AttnSeqs s{pre.data(), meta.data()};
+  for (int b = 0; b < n; ++b) CHECK(s.len(b) == lens[b] && s.row(b) == b, "meta %d", b);
+  const long long total = (long long)pre[n] * heads;
+  const int ctas = attn_ctas(total, grid, W);
+  CHECK(total > 0 || ctas == 0, "empty call has CTAs");
+  ++cases;
+  std::map<long long, int> written;                       // unit -> times written
+  std::map<int, std::pair<long long, int>> counter;       // counter -> unit, arrivals
+  std::map<long long, std::set<int>> far;                 // unit -> CTAs that left a part
+  long long expect_b = 0, expect_h = 0, expect_t = -1;    // the line in order
+  int eb = -1;
+  for (int c = 0; c < ctas; ++c) {
+    const long long s0 = range_start(total, c, ctas), s1 = range_start(total, c + 1, ctas);
+    CHECK(s1 > s0, "empty CTA");
+    std::vector<long long> part(2 * W, -1);
+    for (int w = 0; w < W; ++w) {
+      const long long w0 = s0 + range_start(s1 - s0, w, W), w1 = s0 + range_start(s1 - s0, w + 1, W);
+      if (w0 >= w1) continue;
+      AttnCursor cur;
+      cur.set(s, n, heads, w0);
+      bool from_start = cur.t == 0;
+      for (long long g = w0; g < w1; ++g) {
+        // the place is the next one of the line
+        if (expect_t >= 0) {
+          if (++expect_t == s.tiles(eb)) {
+            expect_t = 0;
+            if (++expect_h == heads) {
+              expect_h = 0;
+              do ++eb; while (eb < n && s.tiles(eb) == 0);
+            }
+          }
+        } else {
+          expect_t = 0;
+          eb = 0;
+          while (s.tiles(eb) == 0) ++eb;
+        }
+        CHECK(cur.b == eb && cur.h == expect_h && cur.t == expect_t && cur.nt == s.tiles(eb), "place %lld", g);
+        CHECK(cur.b < n && cur.t * kAttnTile < lens[cur.b], "beyond a request");
+        const bool ue = cur.t == cur.nt - 1, re = g == w1 - 1;
+        if (ue || re) {
+          if (ue && from_start) written[cur.unit(heads)]++;
+          else {
+            const int slot = re ? 1 : 0;
+            CHECK(part[2 * w + slot] < 0, "part slot twice");
+            part[2 * w + slot] = cur.unit(heads);
+          }
+          from_start = true;
+        }
+        if (!re) cur.next(s, n, heads);
+      }
+    }
+    bool used[2] = {false, false};
+    for (int a = 0; a < 2 * W;) {
+      if (part[a] < 0) { ++a; continue; }
+      const long long unit = part[a];
+      int e = a + 1;
+      while (e < 2 * W && (part[e] < 0 || part[e] == unit)) ++e;
+      const int b = (int)(unit / heads), h = (int)(unit % heads);
+      const long long u0 = (long long)pre[b] * heads + (long long)h * s.tiles(b), u1 = u0 + s.tiles(b);
+      if (u0 >= s0 && u1 <= s1) written[unit]++;
+      else {
+        const int slot = u0 >= s0;
+        CHECK(!used[slot], "workspace slot twice");
+        used[slot] = true;
+        const int c0 = range_of(u0, total, ctas), c1 = range_of(u1 - 1, total, ctas);
+        CHECK(c0 <= c && c <= c1 && c1 > c0, "CTAs of a unit");
+        CHECK((slot == 1) == (c == c0), "slot of the first CTA");
+        CHECK(far[unit].insert(c).second, "two parts of a unit in one CTA");
+        auto& k = counter[c0];
+        if (k.second == 0) k.first = unit;
+        CHECK(k.first == unit, "counter shared");
+        if (++k.second == c1 - c0 + 1) written[unit]++;
+      }
+      a = e;
+    }
+  }
+  split_units += (long long)far.size();
+  for (auto& k : counter)
+    CHECK((int)far[k.second.first].size() == k.second.second, "arrivals");
+  for (int b = 0; b < n; ++b)
+    for (int h = 0; h < heads; ++h) {
+      const auto it = written.find((long long)b * heads + h);
+      CHECK((it == written.end() ? 0 : it->second) == (s.tiles(b) ? 1 : 0), "unit %d %d written", b, h);
+    }
+}
+
+int main() {
+  std::mt19937 r(7);
+  auto u = [&](int a, int b) { return a + (int)(r() % (unsigned)(b - a + 1)); };
+  for (int W : {4, 8})
+    for (int len : {0, 1, 15, 16, 17, 127, 128, 512, 4096, 40000})
+      for (int heads : {1, 8})
+        walk({len}, heads, 148, W);
+  for (int i = 0; i < 400; ++i) {
+    const int n = u(1, i % 10 ? 40 : 600), heads = u(1, i % 7 ? 8 : 64), most = 1 << u(2, 12);
+    std::vector<int> lens(n);
+    for (auto& l : lens) l = u(0, 4) ? u(0, most) : 0;
+    walk(lens, heads, i % 3 ? 148 : u(1, 160), u(0, 1) ? 8 : 4);
+  }
+  // ranges far beyond 32 bits
+  for (int i = 0; i < 2000; ++i) {
+    const long long total = ((long long)r() << 9) + r() % 1000 + 1;
+    const int n = u(1, 148);
+    if (total < n) continue;
+    const int c = u(0, n - 1);
+    const long long a = range_start(total, c, n), b = range_start(total, c + 1, n);
+    CHECK(a < b && range_of(a, total, n) == c && range_of(b - 1, total, n) == c, "range of %lld", total);
+  }
+  printf("cases=%lld split=%lld bad=%lld\n", cases, split_units, bad);
+  return bad ? 1 : 0;
+}
+"""
+
+
+def test_every_tile_once_and_every_unit_written_once(tmp_path):
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    src, exe = tmp_path / "split.cpp", tmp_path / "split"
+    src.write_text(HARNESS)
+    hdr = tmp_path / "attn_split.cuh"
+    hdr.write_text(open(os.path.join(svq_build.CSRC, "attn_split.cuh")).read())
+    r = subprocess.run([cxx, "-O1", "-std=c++17", "-I", str(tmp_path), str(src), "-o", str(exe)], capture_output=True,
+                       text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout
+    counts = dict(kv.split("=") for kv in r.stdout.split())
+    assert int(counts["cases"]) > 400 and int(counts["split"]) > 1000
