@@ -576,6 +576,9 @@ int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_
   p.n_seqs = n_seqs; p.width = max_pages; p.n_q = n_q_heads; p.n_rows = n_rows;
   p.group = n_q_heads / cache->n_heads;
   p.row_tiles = (p.group + plan.rows - 1) / plan.rows;
+  p.by_heads = svq::FastDiv(cache->n_heads * p.row_tiles);
+  p.by_row_tiles = svq::FastDiv(p.row_tiles);
+  p.by_page = svq::FastDiv(cache->page_size);
   p.out_bf16 = out_dtype == SVQ_BF16;
   return cuda_status(svq::launch_paged_attn(p, plan, cache->head_dim, cache->dtype == SVQ_BF16, (cudaStream_t)stream));
 }

@@ -8,6 +8,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "attn_split.cuh"
+
 namespace svq {
 
 constexpr int kMaxSeqs = 4096;           // requests of one call (their prefix sums stay in shared memory)
@@ -71,6 +73,7 @@ struct PagedAttnParams {
   float* warp_part;                      // [ctas][warps][rows * D]
   KvView kv;
   float scale_log2;
+  FastDiv by_heads, by_row_tiles, by_page;   // key heads * row tiles, row tiles, tokens per page
   int n_seqs, width, n_q, n_rows, group, row_tiles, out_bf16;
 };
 

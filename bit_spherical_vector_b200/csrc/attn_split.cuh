@@ -15,10 +15,38 @@ namespace svq {
 
 constexpr int kAttnTile = 16;            // keys per tile
 
-// First place of range i of n over places [0, total).
-SVQ_HD long long range_start(long long total, int i, int n) { return total * i / n; }
-// The range that place g lies in: the last i with range_start(i) <= g.
-SVQ_HD int range_of(long long g, long long total, int n) { return (int)(((g + 1) * n - 1) / total); }
+// Quotient of nonnegative numbers: a 64-bit division is ten times a 32-bit one
+// and only lines beyond 2^32 tiles need it.
+SVQ_HD long long div_places(long long a, long long b) {
+  if (((unsigned long long)a | (unsigned long long)b) >> 32 == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
+// Quotient of a number below 2^31 by a divisor that the host knows: with m =
+// floor(2^(31 + s) / d) + 1 and 2^(s - 1) < d <= 2^s the product's high part is
+// exact (T. Granlund and P. Montgomery, Division by Invariant Integers using
+// Multiplication, 1994).
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+  FastDiv() = default;
+  explicit FastDiv(int divisor) : d((uint32_t)divisor), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)((1ull << (31 + s)) / d + 1);
+  }
+  SVQ_HD int div(int n) const { return (int)(((unsigned long long)(uint32_t)n * m) >> (31 + s)); }
+};
+
+// Places [0, total) in n ranges of equal size, the first ranges one longer.
+struct AttnLine {
+  long long size, longer;                // size of the shorter ranges, how many are longer
+  SVQ_HD AttnLine(long long total, int n) : size(div_places(total, n)), longer(total - size * n) {}
+  SVQ_HD long long start(int i) const { return size * i + (i < longer ? i : longer); }
+  SVQ_HD int range_of(long long g) const {             // the range that place g lies in
+    const long long split = longer * (size + 1);
+    return (int)(g < split ? div_places(g, size + 1) : longer + div_places(g - split, size));
+  }
+};
 
 // CTAs that take part: each of their warps gets a tile at least.
 SVQ_HD int attn_ctas(long long total, int grid, int warps) {
@@ -39,8 +67,8 @@ struct AttnSeqs {
 // A place on the line: tile t of nt of head (and row tile) h of request b.
 struct AttnCursor {
   int b, h, t, nt;
-  SVQ_HD void set(const AttnSeqs& s, int n, int heads, long long g) {
-    const int gq = (int)(g / heads);
+  SVQ_HD void set(const AttnSeqs& s, int n, int heads, const FastDiv& by_heads, long long g) {
+    const int gq = g >> 31 ? (int)(g / heads) : by_heads.div((int)g);
     int lo = 0, hi = n;
     while (hi - lo > 1) {                // last b with pre[b] <= gq: a request with tiles
       const int mid = (lo + hi) >> 1;
@@ -49,19 +77,10 @@ struct AttnCursor {
     b = lo;
     nt = s.tiles(b);
     const long long r = g - (long long)s.pre[b] * heads;
-    h = (int)(r / nt);
+    h = (int)div_places(r, nt);
     t = (int)(r - (long long)h * nt);
   }
-  // The next place; called only where there is one.
-  SVQ_HD void next(const AttnSeqs& s, int n, int heads) {
-    if (++t < nt) return;
-    t = 0;
-    if (++h < heads) return;
-    h = 0;
-    do ++b; while (b < n && s.tiles(b) == 0);
-    nt = b < n ? s.tiles(b) : 1;
-  }
-  SVQ_HD long long unit(int heads) const { return (long long)b * heads + h; }
+  SVQ_HD int unit(int heads) const { return b * heads + h; }   // at most 2^22
 };
 
 }  // namespace svq

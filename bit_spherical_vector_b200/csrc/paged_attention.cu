@@ -123,21 +123,39 @@ __device__ __forceinline__ float ex2(float x) {
 // log2): a part that saw no key has m = -inf and weight 0.
 __device__ __forceinline__ float part_weight(float m, float M) { return m == kNegInf ? 0.f : ex2(m - M); }
 
+// Where a unit's result goes: row of the output, first query head << 8 | heads,
+// and the CTAs that share the unit.
+struct UnitOut {
+  int row, heads, c0, c1;
+};
+
+__device__ __forceinline__ void weigh(float4& acc, float f, const float4& v) {
+  acc.x = fmaf(v.x, f, acc.x);
+  acc.y = fmaf(v.y, f, acc.y);
+  acc.z = fmaf(v.z, f, acc.z);
+  acc.w = fmaf(v.w, f, acc.w);
+}
+
 template <int D, int NQ, bool BF16>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
   using S = Shape<D>;
   constexpr int W = S::kWarps, T = S::kThreads, R = NQ * 8;        // R: query heads per unit, padded
   constexpr int KS = D / 16;                                       // 16-wide steps along a head
   constexpr int CPR = D / 8;                                       // 16-byte chunks of a key
+  constexpr int kPitch = D + 4;                                    // floats between heads of a warp's part
+  constexpr int kPartWords = R * D + 2 * R;                        // a CTA's part: entries, then (maximum, sum) pairs
   constexpr float kShift = BF16 ? 0.f : 15.f;                      // P is kept 2^kShift times as large
   extern __shared__ __align__(128) unsigned char smem[];
   int* pre = reinterpret_cast<int*>(smem + S::kRing);
   uint32_t* meta = reinterpret_cast<uint32_t*>(pre + p.n_seqs + 1);
-  __shared__ float part_m[W][2][R], part_l[W][2][R];
-  __shared__ long long part_unit[W][2];                            // unit of a part, -1: none
-  __shared__ uint32_t live[W][S::kStages];                         // keys of a stage that count
+  constexpr int P = 2 * W;                                         // parts of a CTA at most: two per warp
+  static_assert(P * R <= T, "one thread for each part and head");
+  __shared__ float2 part_ml[P][R];                                 // (maximum, sum) of a part
+  __shared__ UnitOut part_to[P];
+  __shared__ int part_unit[P];                                     // unit of a part, -1: none
+  __shared__ int2 note[W][S::kStages];                             // tile in a stage: keys that count and flags; unit
   __shared__ int wsum[W];
-  __shared__ unsigned joined[2];
+  __shared__ bool joined[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.n_seqs, heads = p.kv.n_heads * p.row_tiles;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -204,165 +222,150 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   const int ctas = attn_ctas(total, gridDim.x, W);
   const int cta = blockIdx.x;
   if (cta >= ctas) return;
-  const long long s0 = range_start(total, cta, ctas), s1 = range_start(total, cta + 1, ctas);
-  const long long w0 = s0 + range_start(s1 - s0, warp, W), w1 = s0 + range_start(s1 - s0, warp + 1, W);
+  const AttnLine line(total, ctas);
+  const long long s0 = line.start(cta), s1 = line.start(cta + 1);
+  const AttnLine part(s1 - s0, W);
+  const long long w0 = s0 + part.start(warp), w1 = s0 + part.start(warp + 1);
 
   const uint32_t ring = sm100::smem_u32(smem) + warp * S::kStages * S::kStage;
-  float o[KS][NQ][4];
-  float mx[NQ][2], ls[NQ][2];
-  uint32_t qf[KS][NQ][2];
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
-  if (lane < 2) part_unit[warp][lane] = -1;
+  if (lane < 2) part_unit[2 * warp + lane] = -1;
 
-  // Writes the running part of unit (b, h) of this warp: slot 0 to the
-  // workspace in mid-range (the ring is in use), slot 1 to the drained ring.
-  auto leave_part = [&](const AttnCursor& c, int slot) {
-    float* dst = slot == 0 ? p.warp_part + ((int64_t)cta * W + warp) * R * D
-                           : reinterpret_cast<float*>(smem + (size_t)warp * S::kStages * S::kStage);
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-#pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const int d = i * 16 + g8, r = q * 8 + t2;
-        dst[r * D + d] = o[i][q][0];
-        dst[(r + 1) * D + d] = o[i][q][1];
-        dst[r * D + d + 8] = o[i][q][2];
-        dst[(r + 1) * D + d + 8] = o[i][q][3];
-      }
-      if (g8 == 0) {
-        part_m[warp][slot][q * 8 + t2] = mx[q][0];
-        part_m[warp][slot][q * 8 + t2 + 1] = mx[q][1];
-        part_l[warp][slot][q * 8 + t2] = ls[q][0];
-        part_l[warp][slot][q * 8 + t2 + 1] = ls[q][1];
-      }
-    }
-    if (lane == 0) part_unit[warp][slot] = c.unit(heads);
-  };
-  // Heads of a unit: first query head and how many of the R rows are real.
-  auto unit_heads = [&](int h, int* count) {
-    const int kv_head = h / p.row_tiles, rt = h - kv_head * p.row_tiles;
-    *count = min(R, p.group - rt * R);
-    return kv_head * p.group + rt * R;
-  };
-  auto put = [&](int64_t row, int head, int d, float v) {
-    const int i = head * D + d;
-    int at = i;
-    if (p.order) {
-      at = p.order[i];
-      if ((unsigned)at >= (unsigned)(p.n_q * D)) {
-        *p.status = SVQ_ERR_INVALID_ARG;
-        return;
-      }
-    }
-    p.out[row * p.n_q * D + at] = out16(v, p.out_bf16);
+  auto put = [&](int64_t row, int i, float v) {            // entry i of the row, in o's order
+    const int at = p.order[i];
+    if ((unsigned)at < (unsigned)(p.n_q * D)) p.out[row * p.n_q * D + at] = out16(v, p.out_bf16);
+    else *p.status = SVQ_ERR_INVALID_ARG;
   };
   auto log_sum = [](float m, float l) {
     return l == 0.f ? kNegInf : fmaf(m - kShift, 0.6931471805599453f, logf(l));
   };
-  // A unit that lies wholly inside this warp's range goes straight out.
-  auto write_unit = [&](const AttnCursor& c) {
-    int count;
-    const int head0 = unit_heads(c.h, &count);
-    const int64_t row = seqs.row(c.b);
+  auto put4 = [&](int64_t row, int head, int d, float2 ml, const float4& acc) {
+    const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
+    const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    const int i = head * D + d;
+    if (p.order) {
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const float i0 = ls[q][0] == 0.f ? 0.f : 1.f / ls[q][0], i1 = ls[q][1] == 0.f ? 0.f : 1.f / ls[q][1];
-      const int r = q * 8 + t2;
-      if (p.order) {
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const int d = i * 16 + g8;
-          if (r < count) {
-            put(row, head0 + r, d, o[i][q][0] * i0);
-            put(row, head0 + r, d + 8, o[i][q][2] * i0);
-          }
-          if (r + 1 < count) {
-            put(row, head0 + r + 1, d, o[i][q][1] * i1);
-            put(row, head0 + r + 1, d + 8, o[i][q][3] * i1);
-          }
-        }
-      } else {
-        // 8 x 8 transposes turn (entry, two heads) into (head, two entries): 4-byte stores
-        const int rr = q * 8 + g8;
-        uint16_t* dst = p.out + (row * p.n_q + head0 + rr) * D + t2;
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const uint32_t lo = p.out_bf16 ? pack2<true>(o[i][q][0] * i0, o[i][q][1] * i1)
-                                         : pack2<false>(o[i][q][0] * i0, o[i][q][1] * i1);
-          const uint32_t hi = p.out_bf16 ? pack2<true>(o[i][q][2] * i0, o[i][q][3] * i1)
-                                         : pack2<false>(o[i][q][2] * i0, o[i][q][3] * i1);
-          const uint32_t a = transpose8(lo), b = transpose8(hi);
-          if (rr < count) {
-            *reinterpret_cast<uint32_t*>(dst + i * 16) = a;
-            *reinterpret_cast<uint32_t*>(dst + i * 16 + 8) = b;
-          }
-        }
-      }
-      if (p.lse && g8 == 0) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (r + e < count)
-            p.lse[row * p.n_q + head0 + r + e] = log_sum(mx[q][e], ls[q][e]);
-      }
+      for (int e = 0; e < 4; ++e) put(row, i + e, v[e]);
+    } else {
+      const uint2 w = p.out_bf16 ? make_uint2(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]))
+                                 : make_uint2(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]));
+      *reinterpret_cast<uint2*>(p.out + row * p.n_q * D + i) = w;
     }
+    if (p.lse && d == 0) p.lse[row * p.n_q + head] = log_sum(ml.x, ml.y);
   };
 
-  if (w0 < w1) {
-    // ---- this warp's stream of tiles
-    AttnCursor put_c, get_c;                                   // next tile to load, next tile to use
-    get_c.set(seqs, n, heads, w0);
-    put_c = get_c;
-    const int todo = (int)(w1 - w0);
-    int loaded = 0;                                        // tiles whose loads have been issued
-    int page, off;                                         // of key (lane & 15) of the next tile to load
-    bool in;
-    auto look_up = [&]() {
-      const int key = put_c.t * kTile + (lane & 15);
-      const int j = key / p.kv.page_size;
-      off = key - j * p.kv.page_size;
-      in = key < seqs.len(put_c.b);
-      page = in ? __ldg(p.table + (int64_t)put_c.b * p.width + j) : 0;
-    };
-    auto load_tile = [&](int stage) {
-      if (loaded < todo) {
-        const bool ok = in && (unsigned)page < (unsigned)p.kv.n_pages;
-        if (in && !ok) *p.status = SVQ_ERR_INVALID_ARG;    // a key on a page that does not exist does not count
-        const uint32_t okm = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
-        const int64_t base =
-            ok ? (int64_t)page * p.kv.page_stride + (int64_t)off * p.kv.token_stride : (int64_t)0;
-        const uint16_t* kh = p.kv.k + (int64_t)(put_c.h / p.row_tiles) * p.kv.head_stride;
-        const uint16_t* vh = p.kv.v + (int64_t)(put_c.h / p.row_tiles) * p.kv.head_stride;
-        const uint32_t dst = ring + stage * S::kStage;
-        const int chunk = lane % CPR;
-#pragma unroll
-        for (int i = 0; i < kTile * CPR / 32; ++i) {
-          const int r = i * (32 / CPR) + lane / CPR;
-          const int64_t a = __shfl_sync(0xFFFFFFFFu, base, r) + chunk * 8;
-          const int bytes = (okm >> r) & 1 ? 16 : 0;       // 0: the row is filled with zeros
-          const uint32_t d = dst + r * S::kRow + ((chunk ^ (r & 7)) << 4);
-          cp_async16(d, kh + a, bytes);
-          cp_async16(d + kTile * S::kRow, vh + a, bytes);
-        }
-        if (lane == 0) live[warp][stage] = okm;
-        if (++loaded < todo) {
-          put_c.next(seqs, n, heads);
-          look_up();
+  const int todo = (int)(w1 - w0);
+  if (todo > 0) {
+    // ---- this warp's stream of tiles.  Every 32 tiles each lane finds the place of
+    // one of them: request, head and tile, its first page and the keys that count.
+    const bool whole = p.kv.page_size % kTile == 0;        // a tile lies in one page
+    int64_t at_base = 0;                                   // of lane's tile: element of its first key (or of its head)
+    int at_key = 0, at_req = 0, at_unit = 0, at_info = 0;  // info: keys | unit begins << 8 | unit ends << 9
+    auto look_up = [&](int first) {
+      if (first + lane >= todo) return;
+      AttnCursor c;
+      c.set(seqs, n, heads, p.by_heads, w0 + first + lane);
+      at_key = c.t * kTile;
+      at_req = c.b;
+      at_unit = c.unit(heads);
+      at_base = (int64_t)p.by_row_tiles.div(c.h) * p.kv.head_stride;
+      int keys = min(kTile, seqs.len(c.b) - at_key);
+      if (whole) {
+        const int j = p.by_page.div(at_key);
+        const int page = __ldg(p.table + (int64_t)c.b * p.width + j);
+        if ((unsigned)page < (unsigned)p.kv.n_pages) {
+          at_base += (int64_t)page * p.kv.page_stride + (int64_t)(at_key - j * p.kv.page_size) * p.kv.token_stride;
+        } else {                                           // keys on a page that does not exist do not count
+          keys = 0;
+          *p.status = SVQ_ERR_INVALID_ARG;
         }
       }
-      cp_commit();
+      at_info = keys | (c.t == 0) << 8 | (c.t == c.nt - 1) << 9;
     };
-    look_up();
+    constexpr int kStep = 32 / CPR;                        // keys copied by one instruction of the warp
+    const int chunk = lane % CPR, r_lane = lane / CPR;
+    auto load_tile = [&](int i, int stage) {               // tile i of the range
+      const int src = i & 31;
+      const int64_t base = __shfl_sync(0xFFFFFFFFu, at_base, src) + chunk * 8;
+      const int keys = __shfl_sync(0xFFFFFFFFu, at_info, src) & 255;
+      const uint32_t dst = ring + stage * S::kStage + r_lane * S::kRow;
+      uint32_t okm;
+      if (whole) {
+        okm = (1u << keys) - 1u;
+        const int64_t step = kStep * p.kv.token_stride;
+        int64_t a = base + r_lane * p.kv.token_stride;
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) load_tile(i);
+        for (int r = 0; r < kTile; r += kStep) {
+          const bool in = r + r_lane < keys;               // else the row is filled with zeros, and nothing is read
+          const int64_t e = in ? a : 0;
+          const uint32_t d = dst + r * S::kRow + ((chunk ^ ((r + r_lane) & 7)) << 4);
+          cp_async16(d, p.kv.k + e, in ? 16 : 0);
+          cp_async16(d + kTile * S::kRow, p.kv.v + e, in ? 16 : 0);
+          a += step;
+        }
+      } else {                                             // each key looks its own page up
+        const int key = __shfl_sync(0xFFFFFFFFu, at_key, src) + (lane & 15);
+        const int req = __shfl_sync(0xFFFFFFFFu, at_req, src), j = p.by_page.div(key);
+        int64_t mine = 0;
+        bool ok = false;
+        if ((lane & 15) < keys) {
+          const int page = __ldg(p.table + (int64_t)req * p.width + j);
+          ok = (unsigned)page < (unsigned)p.kv.n_pages;
+          if (ok) mine = (int64_t)page * p.kv.page_stride + (int64_t)(key - j * p.kv.page_size) * p.kv.token_stride;
+          else *p.status = SVQ_ERR_INVALID_ARG;
+        }
+        okm = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
+#pragma unroll
+        for (int r = 0; r < kTile; r += kStep) {
+          const int64_t key_at = __shfl_sync(0xFFFFFFFFu, mine, r + r_lane);
+          const bool in = (okm >> (r + r_lane)) & 1;
+          const int64_t e = in ? base + key_at : 0;
+          const uint32_t d = dst + r * S::kRow + ((chunk ^ ((r + r_lane) & 7)) << 4);
+          cp_async16(d, p.kv.k + e, in ? 16 : 0);
+          cp_async16(d + kTile * S::kRow, p.kv.v + e, in ? 16 : 0);
+        }
+      }
+      if (lane == src) note[warp][stage] = make_int2((at_info & 0x300) << 8 | (int)okm, at_unit);
+    };
 
+    float o[KS][NQ][4];
+    float mx[NQ][2], ls[NQ][2];
+    uint32_t qf[KS][NQ][2];
+    UnitOut to;
     bool fresh = true;                                     // a unit begins here (for this warp)
-    bool from_start = get_c.t == 0;                        // this warp has the unit from its first tile on
-    int stage = 0;
-    for (int i = 0; i < todo; ++i) {
+    bool from_start = true;                                // this warp has the unit from its first tile on
+    int use = 0, put_stage = 0;
+    for (int i = 1 - S::kStages; i < todo; ++i) {
+      // tile i is used, tile i + kStages - 1 goes into the stage that tile i - 1 has left
+      cp_wait<S::kStages - 2>();
+      __syncwarp();
+      const int next = i + S::kStages - 1;
+      if (next < todo) {
+        if ((next & 31) == 0) look_up(next);
+        load_tile(next, put_stage);
+      }
+      cp_commit();
+      put_stage = put_stage + 1 == S::kStages ? 0 : put_stage + 1;
+      if (i < 0) continue;
+      const int2 nb = note[warp][use];
+      const uint32_t okm = (uint32_t)nb.x & 0xFFFFu;
+      const int unit = nb.y;
+      const uint32_t kt = ring + use * S::kStage, vt = kt + kTile * S::kRow;
+      use = use + 1 == S::kStages ? 0 : use + 1;
       if (fresh) {
-        int count;
-        const int head0 = unit_heads(get_c.h, &count);
-        const uint16_t* qr = p.q + ((int64_t)seqs.row(get_c.b) * p.n_q + head0) * D;
+        // what is known of the unit, worked out while its first keys are on their way
+        const int b = p.by_heads.div(unit), h = unit - b * heads, kv_head = p.by_row_tiles.div(h);
+        const int rt = h - kv_head * p.row_tiles, nt = seqs.tiles(b);
+        const int count = min(R, p.group - rt * R);
+        const long long u0 = (long long)seqs.pre[b] * heads + (long long)h * nt, u1 = u0 + nt;
+        to.row = seqs.row(b);
+        to.heads = (kv_head * p.group + rt * R) << 8 | count;
+        to.c0 = to.c1 = cta;
+        if (u0 < s0 || u1 > s1) {
+          to.c0 = line.range_of(u0);
+          to.c1 = line.range_of(u1 - 1);
+        }
+        const uint16_t* qr = p.q + ((int64_t)to.row * p.n_q + (to.heads >> 8)) * D;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           const int r = q * 8 + g8;
@@ -382,17 +385,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[ks][q][e] = 0.f;
         }
+        from_start = (nb.x >> 16) & 1;
         fresh = false;
       }
-      cp_wait<S::kStages - 2>();
-      __syncwarp();
-      const uint32_t okm = live[warp][stage];
-      {
-        const int ahead = stage == 0 ? S::kStages - 1 : stage - 1;   // the stage used one tile ago
-        load_tile(ahead);
-      }
-      const uint32_t kt = ring + stage * S::kStage, vt = kt + kTile * S::kRow;
-      stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
       // scores of 16 keys: rows g8 and g8 + 8, query heads t2 and t2 + 1
       float sc[NQ][4];
@@ -463,145 +458,239 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
         }
       }
 
-      const bool unit_ends = get_c.t == get_c.nt - 1, range_ends = i == todo - 1;
-      if (unit_ends || range_ends) {
+      const bool unit_ends = (nb.x >> 17) & 1, range_ends = i == todo - 1;
+      if (!unit_ends && !range_ends) continue;
+      fresh = true;
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
+      for (int q = 0; q < NQ; ++q)
 #pragma unroll
-          for (int x = 4; x < 32; x <<= 1) {
-            ls[q][0] += __shfl_xor_sync(0xFFFFFFFFu, ls[q][0], x);
-            ls[q][1] += __shfl_xor_sync(0xFFFFFFFFu, ls[q][1], x);
-          }
-        if (unit_ends && from_start) {
-          write_unit(get_c);
-        } else if (range_ends) {
-          cp_wait<0>();
-          __syncwarp();                                    // every lane is done with the ring
-          leave_part(get_c, 1);
-        } else {
-          leave_part(get_c, 0);
+        for (int x = 4; x < 32; x <<= 1) {
+          ls[q][0] += __shfl_xor_sync(0xFFFFFFFFu, ls[q][0], x);
+          ls[q][1] += __shfl_xor_sync(0xFFFFFFFFu, ls[q][1], x);
         }
-        fresh = true;
-        from_start = true;
+      if (!(unit_ends && from_start)) {
+        // A part: in mid-range (the ring is in use) to the workspace, else to the
+        // ring, which is drained: every tile of the range has been waited for.
+        const int slot = range_ends;
+        float* dst = slot ? reinterpret_cast<float*>(smem + (size_t)warp * S::kStages * S::kStage)
+                          : p.warp_part + ((int64_t)cta * W + warp) * R * kPitch;
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+          float* d0 = dst + (q * 8 + t2) * kPitch + g8;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            d0[ks * 16] = o[ks][q][0];
+            d0[ks * 16 + kPitch] = o[ks][q][1];
+            d0[ks * 16 + 8] = o[ks][q][2];
+            d0[ks * 16 + 8 + kPitch] = o[ks][q][3];
+          }
+          if (g8 == 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) part_ml[2 * warp + slot][q * 8 + t2 + e] = make_float2(mx[q][e], ls[q][e]);
+          }
+        }
+        if (lane == 0) {
+          part_unit[2 * warp + slot] = unit;
+          part_to[2 * warp + slot] = to;
+        }
+        continue;
       }
-      if (!range_ends) get_c.next(seqs, n, heads);
+      // The whole unit is this warp's: it goes straight out.
+      const int head0 = to.heads >> 8, count = to.heads & 255;
+      const int64_t row = to.row;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const float i0 = ls[q][0] == 0.f ? 0.f : 1.f / ls[q][0], i1 = ls[q][1] == 0.f ? 0.f : 1.f / ls[q][1];
+        const int r = q * 8 + t2;
+        if (p.order) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (r + (e & 1) < count)
+                put(row, (head0 + r + (e & 1)) * D + ks * 16 + g8 + (e >> 1) * 8, o[ks][q][e] * (e & 1 ? i1 : i0));
+          }
+        } else {
+          // 8 x 8 transposes turn (entry, two heads) into (head, two entries): 4-byte stores
+          const int rr = q * 8 + g8;
+          uint16_t* dst = p.out + (row * p.n_q + head0 + rr) * D + t2;
+#pragma unroll
+          for (int x = 0; x < 2 * KS; ++x) {
+            const float u = o[x >> 1][q][2 * (x & 1)] * i0, w = o[x >> 1][q][2 * (x & 1) + 1] * i1;
+            const uint32_t t = transpose8(p.out_bf16 ? pack2<true>(u, w) : pack2<false>(u, w));
+            if (rr < count) *reinterpret_cast<uint32_t*>(dst + x * 8) = t;
+          }
+        }
+        if (p.lse && g8 == 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (r + e < count) p.lse[row * p.n_q + head0 + r + e] = log_sum(mx[q][e], ls[q][e]);
+        }
+      }
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
 
   // ---- join the warps' parts.  Parts of one unit are neighbours in the order
-  // (warp, slot); units that reach beyond this CTA leave a part in the workspace.
-  const int part_words = R * D + 2 * R;
-  auto cta_part = [&](int c, int slot) { return p.cta_part + ((int64_t)c * 2 + slot) * part_words; };
-  long long far_unit[2] = {-1, -1};                        // units that other CTAs share, and their CTAs
-  int far_c0[2], far_c1[2];
-  for (int a = 0; a < 2 * W;) {
-    const long long unit = part_unit[a >> 1][a & 1];
-    if (unit < 0) {
-      ++a;
-      continue;
+  // (warp, slot).  Thread (x, r) turns the maximum of head r of part x into its
+  // weight among the parts of its unit; the first of them gets the joined maximum
+  // and sum.  No condition stands before a load, so the loads do not queue.
+  static_assert(R * kPitch * 4 + P * R * 4 <= S::kStages * S::kStage, "weights behind the first warp's part");
+  float* part_w = reinterpret_cast<float*>(smem + S::kStages * S::kStage) - P * R;      // [P][R]
+  {
+    const int x = min(tid / R, P - 1), r = tid % R, u = part_unit[x];
+    float2 ml[P];
+    float M = kNegInf, L = 0.f, f = 0.f;
+#pragma unroll
+    for (int y = 0; y < P; ++y) {
+      const int v = part_unit[y];
+      ml[y] = part_ml[y][r];
+      if (v != u || v < 0) ml[y] = make_float2(kNegInf, 0.f);
+      M = fmaxf(M, ml[y].x);
     }
-    int e = a + 1;
-    while (e < 2 * W && (part_unit[e >> 1][e & 1] < 0 || part_unit[e >> 1][e & 1] == unit)) ++e;
-    const int b = (int)(unit / heads), h = (int)(unit - (long long)b * heads);
-    const long long u0 = (long long)seqs.pre[b] * heads + (long long)h * seqs.tiles(b), u1 = u0 + seqs.tiles(b);
-    int count;
-    const int head0 = unit_heads(h, &count);
-    const bool whole = u0 >= s0 && u1 <= s1;
-    float* far = nullptr;
-    if (!whole) {
-      const int slot = u0 >= s0;                           // 1: the unit begins here, 0: it began before
-      far_unit[slot] = unit;
-      far_c0[slot] = range_of(u0, total, ctas);
-      far_c1[slot] = range_of(u1 - 1, total, ctas);
-      far = cta_part(cta, slot);
+#pragma unroll
+    for (int y = 0; y < P; ++y) {
+      const float g = part_weight(ml[y].x, M);
+      L = fmaf(g, ml[y].y, L);
+      if (y == x) f = g;
     }
-    const int64_t row = seqs.row(b);
-    for (int i = tid; i < count * D; i += T) {
-      const int r = i / D, d = i - r * D;
-      float M = kNegInf;
-      for (int x = a; x < e; ++x)
-        if (part_unit[x >> 1][x & 1] == unit) M = fmaxf(M, part_m[x >> 1][x & 1][r]);
-      float acc = 0.f, L = 0.f;
-      for (int x = a; x < e; ++x) {
-        if (part_unit[x >> 1][x & 1] != unit) continue;
-        const float f = part_weight(part_m[x >> 1][x & 1][r], M);
-        const float v = x & 1 ? reinterpret_cast<const float*>(smem + (size_t)(x >> 1) * S::kStages * S::kStage)[i]
-                              : __ldcg(p.warp_part + ((int64_t)cta * W + (x >> 1)) * R * D + i);
-        acc = fmaf(f, v, acc);
-        L = fmaf(f, part_l[x >> 1][x & 1][r], L);
-      }
-      if (far) {
-        far[i] = acc;
-        if (d == 0) {
-          far[R * D + r] = M;
-          far[R * D + R + r] = L;
-        }
-      } else {
-        put(row, head0 + r, d, L == 0.f ? 0.f : acc / L);
-        if (p.lse && d == 0)
-          p.lse[row * p.n_q + head0 + r] = log_sum(M, L);
-      }
+    __syncthreads();
+    if (tid < P * R) {
+      part_w[x * R + r] = f;
+      part_ml[x][r] = make_float2(M, L);
     }
-    a = e;
+    __syncthreads();
   }
-  if (far_unit[0] < 0 && far_unit[1] < 0) return;
+  const int my_unit = lane < P ? part_unit[lane] : -1;
+  const uint32_t have = __ballot_sync(0xFFFFFFFFu, my_unit >= 0);
+  const uint32_t lower = have & ((1u << lane) - 1u);
+  const int prev = __shfl_sync(0xFFFFFFFFu, my_unit, lower ? 31 - __clz(lower) : lane);
+  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, my_unit >= 0 && (!lower || prev != my_unit));
+  // part x of a unit: CTA c0 + x's, in its place 1 if the unit begins there and else in place 0
+  auto cta_part = [&](const UnitOut& u, int x) { return p.cta_part + ((u.c0 + x) * 2 + (x == 0)) * kPartWords; };
+  int shared_by[2] = {-1, -1};                             // first parts of the units that other CTAs share
+#pragma unroll 1
+  for (uint32_t left = firsts; left; left &= left - 1) {
+    const int a = __ffs(left) - 1;
+    const uint32_t later = left & (left - 1);              // the next unit's first part
+    const uint32_t members = have & ~((1u << a) - 1u) & (later ? (later & (0u - later)) - 1u : ~0u);
+    const UnitOut u = part_to[a];
+    const int count = u.heads & 255;
+    float* far = nullptr;
+    if (u.c0 != u.c1) {
+      shared_by[u.c0 == cta] = a;
+      far = cta_part(u, cta - u.c0);
+    }
+#pragma unroll 1
+    for (int i = tid * 4; i < count * D; i += T * 4) {
+      const int r = i / D, d = i - r * D;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {                        // the parts in the ring
+        const bool in = (members >> (2 * w + 1)) & 1;
+        float4 v = *reinterpret_cast<const float4*>(smem + (size_t)w * S::kStages * S::kStage + (r * kPitch + d) * 4);
+        v = make_float4(in ? v.x : 0.f, in ? v.y : 0.f, in ? v.z : 0.f, in ? v.w : 0.f);
+        weigh(acc, in ? part_w[(2 * w + 1) * R + r] : 0.f, v);
+      }
+#pragma unroll 1
+      for (uint32_t x = members & 0x55555555u; x; x &= x - 1) {      // those left in mid-range
+        const int y = __ffs(x) - 1;
+        weigh(acc, part_w[y * R + r], __ldcg(reinterpret_cast<const float4*>(
+                                     p.warp_part + ((int64_t)cta * W + (y >> 1)) * R * kPitch + r * kPitch + d)));
+      }
+      const float2 ml = part_ml[a][r];
+      if (far) {
+        *reinterpret_cast<float4*>(far + i) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(far + R * D + 2 * r) = ml;
+      } else {
+        put4(u.row, (u.heads >> 8) + r, d, ml, acc);
+      }
+    }
+  }
+  if (shared_by[0] < 0 && shared_by[1] < 0) return;
 
   // ---- join the CTAs' parts: the last of the unit's CTAs to get here adds them.
-  __threadfence();
   __syncthreads();
   if (tid < 2) {
-    unsigned last = 0;
-    const long long unit = tid ? far_unit[1] : far_unit[0];
-    if (unit >= 0) {
-      const int c0 = tid ? far_c0[1] : far_c0[0], c1 = tid ? far_c1[1] : far_c1[0];
-      last = atomicInc(p.counters + c0, (unsigned)(c1 - c0)) == (unsigned)(c1 - c0);    // wraps to zero
-      __threadfence();
+    const int a = tid ? shared_by[1] : shared_by[0];
+    bool last = false;
+    if (a >= 0) {
+      // Release of this CTA's parts (the barrier above puts them before it) and
+      // acquire of the others'; wraps to zero with the last arrival.
+      const unsigned others = (unsigned)(part_to[a].c1 - part_to[a].c0);
+      unsigned old;
+      asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                   : "=r"(old)
+                   : "l"(p.counters + part_to[a].c0), "r"(others)
+                   : "memory");
+      last = old == others;
     }
     joined[tid] = last;
   }
   __syncthreads();
-  float* wts = reinterpret_cast<float*>(smem);             // [parts][R]
+#pragma unroll 1
   for (int s = 0; s < 2; ++s) {
     if (!joined[s]) continue;
-    const int c0 = far_c0[s], c1 = far_c1[s], k = c1 - c0 + 1;
-    const long long unit = far_unit[s];
-    const int b = (int)(unit / heads), h = (int)(unit - (long long)b * heads);
-    int count;
-    const int head0 = unit_heads(h, &count);
-    float* psum = wts + k * R;                             // [parts][R] sums
-    float* sums = psum + k * R;                            // [R] maxima, [R] sums
-    for (int i = tid; i < k * R; i += T) {
-      const float* ml = cta_part(c0 + i / R, i / R == 0) + R * D + i % R;
-      wts[i] = __ldcg(ml);
-      psum[i] = __ldcg(ml + R);
-    }
-    __syncthreads();
-    if (tid < count) {
-      float M = kNegInf, L = 0.f;
-      for (int x = 0; x < k; ++x) M = fmaxf(M, wts[x * R + tid]);
-      for (int x = 0; x < k; ++x) {
-        const float f = part_weight(wts[x * R + tid], M);
-        wts[x * R + tid] = f;
-        L = fmaf(f, psum[x * R + tid], L);
-      }
-      sums[tid] = M;
-      sums[R + tid] = L;
-    }
-    __syncthreads();
-    const int64_t row = seqs.row(b);
-    for (int i = tid; i < count * D; i += T) {
-      const int r = i / D, d = i - r * D;
-      float acc = 0.f;
+    const UnitOut u = part_to[s ? shared_by[1] : shared_by[0]];
+    const int parts = u.c1 - u.c0 + 1, count = u.heads & 255;
+    // Shared memory: the parts' weights, the joined (maximum, sum) of each head,
+    // then as many parts' entries as fit, copied there all at once.
+    float2* ml = reinterpret_cast<float2*>(smem);          // [parts][R], then [R] joined
+    float2* top = ml + parts * R;
+    float* hold = reinterpret_cast<float*>(top + R);
+    constexpr int kPieces = (R * D + 4 * T - 1) / (4 * T);
+    float4 acc[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int words = count * D, fit = (S::kRing - (parts + 1) * R * 8) / (words * 4);
+    for (int first = 0; first < parts; first += fit) {
+      const int now = min(fit, parts - first);
+      const uint32_t hold_at = sm100::smem_u32(hold);
+#pragma unroll 1
+      for (int i = tid * 4; i < words; i += T * 4) {
 #pragma unroll 8
-      for (int x = 0; x < k; ++x) acc = fmaf(wts[x * R + r], __ldcg(cta_part(c0 + x, x == 0) + i), acc);
-      const float L = sums[R + r];
-      put(row, head0 + r, d, L == 0.f ? 0.f : acc / L);
-      if (p.lse && d == 0)
-        p.lse[row * p.n_q + head0 + r] = log_sum(sums[r], L);
+        for (int x = 0; x < now; ++x) cp_async16(hold_at + (x * words + i) * 4, cta_part(u, first + x) + i, 16);
+      }
+      cp_commit();
+      if (first == 0) {
+#pragma unroll 4
+        for (int i = tid; i < parts * R; i += T)
+          ml[i] = __ldcg(reinterpret_cast<const float2*>(cta_part(u, i / R) + R * D) + i % R);
+        __syncthreads();
+        if (tid < R) {
+          float M = kNegInf, L = 0.f;
+#pragma unroll 8
+          for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * R + tid].x);
+#pragma unroll 8
+          for (int x = 0; x < parts; ++x) {
+            const float2 v = ml[x * R + tid];
+            const float f = part_weight(v.x, M);
+            ml[x * R + tid].x = f;
+            L = fmaf(f, v.y, L);
+          }
+          top[tid] = make_float2(M, L);
+        }
+      }
+      cp_wait<0>();
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int i = (tid + k * T) * 4;
+        if (i >= words) break;
+#pragma unroll 8
+        for (int x = 0; x < now; ++x)
+          weigh(acc[k], ml[(first + x) * R + i / D].x, *reinterpret_cast<const float4*>(hold + x * words + i));
+      }
+      __syncthreads();                                     // before the next round's copies
     }
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      const int i = (tid + k * T) * 4;
+      if (i < words) put4(u.row, (u.heads >> 8) + i / D, i % D, top[i / D], acc[k]);
+    }
+    __syncthreads();                                       // before shared memory is used for the other unit
   }
 }
 
@@ -643,7 +732,7 @@ bool plan_paged_attn(int n_q, int n_kv, int head_dim, int n_seqs, int num_sms, P
   const size_t cta_bytes = (size_t)plan->ctas * 2 * (plan->rows * head_dim + 2 * plan->rows) * 4;
   plan->cta_part = kGemvCounterBytes;
   plan->warp_part = (plan->cta_part + cta_bytes + 255) / 256 * 256;
-  plan->ws_total = plan->warp_part + (size_t)plan->ctas * plan->warps * plan->rows * head_dim * 4;
+  plan->ws_total = plan->warp_part + (size_t)plan->ctas * plan->warps * plan->rows * (head_dim + 4) * 4;
   return true;
 }
 

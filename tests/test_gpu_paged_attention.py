@@ -139,6 +139,14 @@ def test_many_ragged_requests(seed):
                page=16))
 
 
+@pytest.mark.parametrize("hq,dim", [(16, 64), (16, 128), (16, 256), (2, 128)])
+def test_most_requests(hq, dim):
+    need_gpu()
+    lens = np.random.default_rng(dim).integers(0, 30, 4096)
+    lens[4095] = 700
+    check(case(hq, [int(l) for l in lens], hq, 1, dim))
+
+
 def test_rows_of_a_step():
     """Requests without a row are left out, a request's query is its last row of the step, other rows keep what
     they held."""

@@ -4,7 +4,7 @@ a host program and walked the way the kernel walks them.
 For seeded batches (one to 600 requests, lengths 0 to thousands, 1 to 64 heads and row tiles, 4 and 8 warps,
 148 CTAs and fewer) every tile of every unit must be visited exactly once, in order; every unit must be
 written exactly once: by the one warp that has all of it, by the one CTA that has all of it, or by the last
-of the CTAs from range_of(first tile) to range_of(last tile), which are exactly the CTAs that leave a part of
+of the CTAs from that of its first tile to that of its last, which are exactly the CTAs that leave a part of
 it; no CTA uses a workspace slot twice, no warp a part slot twice, and a counter (that of the unit's first CTA)
 belongs to one unit and gets as many arrivals as the unit has CTAs.  Places beyond 2^31 are checked on the range
 functions alone."""
@@ -42,22 +42,27 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
   const int ctas = attn_ctas(total, grid, W);
   CHECK(total > 0 || ctas == 0, "empty call has CTAs");
   ++cases;
+  const AttnLine line(total, ctas > 0 ? ctas : 1);
+  const FastDiv by_heads(heads);
   std::map<long long, int> written;                       // unit -> times written
   std::map<int, std::pair<long long, int>> counter;       // counter -> unit, arrivals
   std::map<long long, std::set<int>> far;                 // unit -> CTAs that left a part
   long long expect_b = 0, expect_h = 0, expect_t = -1;    // the line in order
   int eb = -1;
   for (int c = 0; c < ctas; ++c) {
-    const long long s0 = range_start(total, c, ctas), s1 = range_start(total, c + 1, ctas);
+    const long long s0 = line.start(c), s1 = line.start(c + 1);
+    const AttnLine share(s1 - s0, W);
     CHECK(s1 > s0, "empty CTA");
     std::vector<long long> part(2 * W, -1);
     for (int w = 0; w < W; ++w) {
-      const long long w0 = s0 + range_start(s1 - s0, w, W), w1 = s0 + range_start(s1 - s0, w + 1, W);
+      const long long w0 = s0 + share.start(w), w1 = s0 + share.start(w + 1);
       if (w0 >= w1) continue;
       AttnCursor cur;
-      cur.set(s, n, heads, w0);
-      bool from_start = cur.t == 0;
+      bool fresh = true, from_start = true;
       for (long long g = w0; g < w1; ++g) {
+        cur.set(s, n, heads, by_heads, g);
+        if (fresh) from_start = cur.t == 0;
+        fresh = false;
         // the place is the next one of the line
         if (expect_t >= 0) {
           if (++expect_t == s.tiles(eb)) {
@@ -82,9 +87,8 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
             CHECK(part[2 * w + slot] < 0, "part slot twice");
             part[2 * w + slot] = cur.unit(heads);
           }
-          from_start = true;
+          fresh = true;
         }
-        if (!re) cur.next(s, n, heads);
       }
     }
     bool used[2] = {false, false};
@@ -100,7 +104,7 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
         const int slot = u0 >= s0;
         CHECK(!used[slot], "workspace slot twice");
         used[slot] = true;
-        const int c0 = range_of(u0, total, ctas), c1 = range_of(u1 - 1, total, ctas);
+        const int c0 = line.range_of(u0), c1 = line.range_of(u1 - 1);
         CHECK(c0 <= c && c <= c1 && c1 > c0, "CTAs of a unit");
         CHECK((slot == 1) == (c == c0), "slot of the first CTA");
         CHECK(far[unit].insert(c).second, "two parts of a unit in one CTA");
@@ -141,8 +145,17 @@ int main() {
     const int n = u(1, 148);
     if (total < n) continue;
     const int c = u(0, n - 1);
-    const long long a = range_start(total, c, n), b = range_start(total, c + 1, n);
-    CHECK(a < b && range_of(a, total, n) == c && range_of(b - 1, total, n) == c, "range of %lld", total);
+    const AttnLine line(total, n);
+    const long long a = line.start(c), b = line.start(c + 1);
+    CHECK(a < b && line.range_of(a) == c && line.range_of(b - 1) == c, "range of %lld", total);
+    CHECK(line.start(0) == 0 && line.start(n) == total, "ends of %lld", total);
+  }
+  // quotients by known divisors, at the ends of their range and around multiples
+  for (int i = 0; i < 200000; ++i) {
+    const int d = i < 5000 ? i + 1 : 1 + (int)(r() >> (1 + r() % 31)) , k = (int)(r() >> 1) / d;
+    const FastDiv f(d);
+    for (long long x : {(long long)k * d - 1, (long long)k * d, (long long)k * d + d - 1, (long long)(r() >> 1), 0x7FFFFFFFll, 0ll})
+      if (x >= 0 && x <= 0x7FFFFFFF) CHECK(f.div((int)x) == x / d, "%lld / %d", x, d);
   }
   printf("cases=%lld split=%lld bad=%lld\n", cases, split_units, bad);
   return bad ? 1 : 0;
