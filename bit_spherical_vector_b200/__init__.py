@@ -119,9 +119,12 @@ def _check(status: int, what: str):
 
 
 def _stream(stream=None):
+    """The handle of a torch stream, or of the current one (the raw handle: building a Stream object takes as
+    long as a launch, 3.2 us against 0.1 us)."""
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ptr(t) -> ctypes.c_void_p:
@@ -365,23 +368,15 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _on_device(what: str, *tensors):
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{what}: tensors must be on the current CUDA device")
-
-
 def _opt(t):
     return None if t is None else t.data_ptr()
 
 
-def _i32(what: str, *tensors):
-    import torch
+def _arrays(what: str, dtype, dev: int, *tensors):
+    """Contiguous arrays of one type on the current device (None: an optional one that is absent)."""
     for t in tensors:
-        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous()):
-            raise ValueError(f"{what}: integer arrays must be contiguous int32")
+        if t is not None and not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+            raise ValueError(f"{what}: an array of {dtype} must be contiguous and on the current CUDA device")
 
 
 class KvCache:
@@ -393,7 +388,7 @@ class KvCache:
               "KvCache: k and v must be alike, [n_pages][page_size][n_heads][head_dim]")
         _need(k.stride(3) == 1, "KvCache: the entries of a head must be contiguous")
         _need(k.get_device() == v.get_device(), "KvCache: k and v must be on one device")
-        self.k, self.v, self.dtype = k, v, k.dtype
+        self.k, self.v, self.dtype, self.device = k, v, k.dtype, k.get_device()
         self.n_pages, self.page_size, self.n_heads, self.head_dim = (int(d) for d in k.shape)
         self.desc = svq_kv_cache(_dtype_code(k.dtype), self.n_pages, self.page_size, self.n_heads, self.head_dim, 0,
                                  k.stride(0), k.stride(1), k.stride(2), k.data_ptr(), v.data_ptr())
@@ -409,7 +404,7 @@ class Rope:
         _need(inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous() and inv_freq.is_cuda,
               "Rope: inv_freq must be a contiguous fp64 vector on the device")
         self.inv_freq, self.interleaved, self.factor = inv_freq, bool(interleaved), float(factor)
-        self.rot_dim = 2 * inv_freq.numel()
+        self.rot_dim, self.device = 2 * inv_freq.numel(), inv_freq.get_device()
         self.desc = svq_rope(inv_freq.data_ptr(), self.rot_dim, int(self.interleaved), self.factor, 0)
         self._ref = ctypes.addressof(self.desc)
 
@@ -436,10 +431,11 @@ def svq_kv_assign(lens, n_new, page_size: int, block_table, free_pages, n_free, 
                   positions, slots, stream=None):
     """Block table, positions and slots of one step from the requests' lengths: request b holds lens[b] tokens and
     gets n_new[b] (negative: it is done).  All int32 on the device; lens_out may be lens, n_free_out may be n_free."""
+    import torch
     what = "svq_kv_assign"
     n, rows = lens.numel(), slots.numel()
-    _i32(what, lens, n_new, block_table, free_pages, n_free, lens_out, n_free_out, cu_rows, positions, slots)
-    _on_device(what, lens, n_new, block_table, free_pages, n_free, lens_out, n_free_out, cu_rows, positions, slots)
+    _arrays(what, torch.int32, torch.cuda.current_device(), lens, n_new, block_table, free_pages, n_free, lens_out,
+            n_free_out, cu_rows, positions, slots)
     _need(block_table.dim() == 2 and block_table.shape[0] == n and n_new.numel() == n and lens_out.numel() == n
           and cu_rows.numel() == n + 1 and positions.numel() == rows and n_free.numel() == 1
           and n_free_out.numel() == 1, f"{what}: sizes do not agree")
@@ -459,13 +455,15 @@ def svq_qk_norm_rope_cache(q, k, v, q_gamma, k_gamma, eps: float, rope: Rope, po
     wq, wk = q_out.shape[1] * D, cache.n_heads * D
     _need(q.shape == (M, wq) and k.shape == (M, wk) and v.shape == (M, wk) and q_out.shape[0] == M
           and q_out.shape[2] == D and positions.numel() == M and slots.numel() == M, f"{what}: sizes do not agree")
-    _need(q.dtype == k.dtype == v.dtype and q_out.dtype == cache.dtype and q_out.is_contiguous()
-          and (M == 0 or q.stride(1) == k.stride(1) == v.stride(1) == 1), f"{what}: types or strides do not agree")
-    for g in (q_gamma, k_gamma):
-        _need(g is None or (g.dtype is torch.float16 and g.numel() == D and g.is_contiguous()),
-              f"{what}: gamma must be fp16 [head_dim]")
-    _i32(what, positions, slots)
-    _on_device(what, q, k, v, q_gamma, k_gamma, rope.inv_freq, positions, slots, cache.k, q_out)
+    _need(q.dtype == k.dtype == v.dtype and (M == 0 or q.stride(1) == k.stride(1) == v.stride(1) == 1), f"{what}: types or strides do not agree")
+    _need((q_gamma is None or q_gamma.numel() == D) and (k_gamma is None or k_gamma.numel() == D),
+          f"{what}: gamma must be [head_dim]")
+    dev = torch.cuda.current_device()
+    _need(q.get_device() == k.get_device() == v.get_device() == rope.device == cache.device == dev,
+          f"{what}: not on the current CUDA device")
+    _arrays(what, torch.int32, dev, positions, slots)
+    _arrays(what, torch.float16, dev, q_gamma, k_gamma)
+    _arrays(what, cache.dtype, dev, q_out)
     ld = (q.stride(0), k.stride(0), v.stride(0)) if M > 1 else (wq, wk, wk)
     _check(lib().svq_qk_norm_rope_cache(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q.dtype), *ld, M,
                                         q_out.shape[1], _opt(q_gamma), _opt(k_gamma), eps, rope._ref,
@@ -491,13 +489,15 @@ def svq_paged_attention(q, cache: KvCache, lens, block_table, scale: float, out,
     n = lens.numel()
     _need(D == cache.head_dim and out.shape == (rows, heads * D) and block_table.dim() == 2
           and block_table.shape[0] == n and (cu_rows.numel() == n + 1 if cu_rows is not None else n <= rows)
-          and (order is None or order.numel() == heads * D)
-          and (lse is None or (lse.shape == (rows, heads) and lse.dtype is torch.float32 and lse.is_contiguous())),
+          and (order is None or order.numel() == heads * D) and (lse is None or lse.shape == (rows, heads)),
           f"{what}: sizes do not agree")
-    _need(q.dtype == cache.dtype and q.is_contiguous() and out.is_contiguous() and ws.is_contiguous(),
-          f"{what}: types or strides do not agree")
-    _i32(what, lens, block_table, cu_rows, order)
-    _on_device(what, q, cache.k, lens, block_table, out, ws, cu_rows, order, lse)
+    dev = torch.cuda.current_device()
+    _need(cache.device == dev, f"{what}: not on the current CUDA device")
+    _arrays(what, cache.dtype, dev, q)
+    _arrays(what, out.dtype, dev, out)
+    _arrays(what, torch.int32, dev, lens, block_table, cu_rows, order)
+    _arrays(what, torch.float32, dev, lse)
+    _arrays(what, ws.dtype, dev, ws)
     _check(lib().svq_paged_attention(q.data_ptr(), rows, heads, cache._ref, lens.data_ptr(), _opt(cu_rows), n,
                                      block_table.data_ptr(), block_table.shape[1], scale, _opt(order),
                                      out.data_ptr(), _dtype_code(out.dtype), _opt(lse), ws.data_ptr(),

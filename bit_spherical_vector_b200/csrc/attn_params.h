@@ -5,6 +5,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -86,6 +87,20 @@ struct PagedAttnPlan {
 bool plan_paged_attn(int n_q, int n_kv, int head_dim, int n_seqs, int num_sms, PagedAttnPlan* plan);
 cudaError_t launch_paged_attn(const PagedAttnParams& p, const PagedAttnPlan& plan, int head_dim, int kv_bf16,
                               cudaStream_t st);
+
+// Lets a kernel use that much dynamic shared memory on the current device.  Set
+// once per device (the call costs a fifth of a launch): `have` is the kernel's own
+// table of what was set.
+template <typename Kern>
+cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<int> (&have)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && have[dev].load(std::memory_order_acquire) >= (int)bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) have[dev].store((int)bytes, std::memory_order_release);
+  return e;
+}
 
 // Launch with programmatic stream serialization (the kernel waits with
 // griddepcontrol.wait) and, for cluster > 1, as clusters of that many CTAs.

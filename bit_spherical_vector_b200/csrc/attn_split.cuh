@@ -40,7 +40,9 @@ struct FastDiv {
 // Places [0, total) in n ranges of equal size, the first ranges one longer.
 struct AttnLine {
   long long size, longer;                // size of the shorter ranges, how many are longer
-  SVQ_HD AttnLine(long long total, int n) : size(div_places(total, n)), longer(total - size * n) {}
+  int n;
+  SVQ_HD AttnLine(long long total, int ranges)
+      : size(div_places(total, ranges)), longer(total - size * ranges), n(ranges) {}
   SVQ_HD long long start(int i) const { return size * i + (i < longer ? i : longer); }
   SVQ_HD int range_of(long long g) const {             // the range that place g lies in
     const long long split = longer * (size + 1);
@@ -48,10 +50,20 @@ struct AttnLine {
   }
 };
 
-// CTAs that take part: each of their warps gets a tile at least.
+// CTAs that take part in an even split: each of their warps gets a tile at least.
 SVQ_HD int attn_ctas(long long total, int grid, int warps) {
   const long long c = (total + warps - 1) / warps;
-  return c < grid ? (int)c : grid;
+  return c < grid ? (c > 0 ? (int)c : 1) : grid;
+}
+
+// Parts of one unit are joined `fan` at a time, level by level; on a level the
+// parts left stand `stride` (a power of fan) apart.  First part of part x's group
+// and the group's size, for a unit of n parts.
+SVQ_HD int attn_group(int n, int fan, int stride, int x, int* members) {
+  const int span = stride * fan, first = x / span * span;
+  const int left = (n - 1 - first) / stride + 1;
+  *members = left < fan ? left : fan;
+  return first;
 }
 
 // The requests of a call as every CTA keeps them: tiles before request b, and
@@ -82,5 +94,22 @@ struct AttnCursor {
   }
   SVQ_HD int unit(int heads) const { return b * heads + h; }   // at most 2^22
 };
+
+// Tiles [s0, s1) of a CTA: one unit (short requests, as many CTAs as units), or
+// its range of the even split.  False: none.
+SVQ_HD bool attn_share(const AttnSeqs& s, int n, int heads, const FastDiv& by_heads, bool by_unit, const AttnLine& line,
+                       int cta, long long* s0, long long* s1) {
+  if (by_unit) {
+    if (cta >= n * heads) return false;
+    const int b = by_heads.div(cta), nt = s.tiles(b);
+    *s0 = (long long)s.pre[b] * heads + (long long)(cta - b * heads) * nt;
+    *s1 = *s0 + nt;
+    return nt > 0;
+  }
+  if (cta >= line.n) return false;
+  *s0 = line.start(cta);
+  *s1 = line.start(cta + 1);
+  return *s1 > *s0;
+}
 
 }  // namespace svq

@@ -196,9 +196,9 @@ __global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_consta
 cudaError_t launch_kv_assign(const KvAssignParams& p, cudaStream_t st) {
   const size_t smem = (size_t)(4 * p.n_seqs + 3) * sizeof(int);
   const unsigned ctas = p.max_rows > 4096 ? 8 : 1;
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kv_assign_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 48 * 1024) {                // the most any call needs, so that concurrent first calls agree
+    static std::atomic<int> have[64];
+    const cudaError_t e = allow_smem(kv_assign_kernel, (size_t)(4 * kMaxSeqs + 3) * sizeof(int), have);
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(kv_assign_kernel, ctas, kThreads, smem, ctas, st, p);

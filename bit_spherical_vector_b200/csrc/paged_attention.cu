@@ -49,6 +49,8 @@ constexpr int kTile = kAttnTile;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr uint32_t kNoRow = ~0u;         // a request without a row in this step
 
+constexpr int kFan = 16;                 // CTAs' parts joined at a time
+
 template <int D>
 struct Shape {
   static constexpr int kWarps = D == 256 ? 4 : 8;
@@ -57,6 +59,11 @@ struct Shape {
   static constexpr int kRow = D * 2;                       // bytes of one key
   static constexpr int kStage = kTile * kRow * 2;          // K tile, then V tile
   static constexpr int kRing = kWarps * kStages * kStage;
+  // A unit of up to 4 tiles per warp is not worth a join: when all are, and there
+  // are CTAs enough, each gets one (three more tiles take a warp as long as the
+  // join of CTAs, about 2 us: 1 request of 512 keys, 8 key heads of 128, 7.7 us
+  // against 8.3 us split over four CTAs each).
+  static constexpr int kUnitTiles = 4 * kWarps;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -161,10 +168,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- prefix sums of the requests' tiles
+  bool any_long, any_empty;                                // requests of more than kUnitTiles tiles, rows without a key
   {
     const int per = (n + T - 1) / T, b0 = min(n, tid * per), b1 = min(n, b0 + per);
     const int most = p.width * p.kv.page_size;
     int sum = 0;
+    bool is_long = false, is_empty = false;
     for (int b = b0; b < b1; ++b) {
       int len = p.lens[b], row = b;
       bool skip = false;
@@ -186,6 +195,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       pre[b] = nt;
       meta[b] = skip ? kNoRow : ((uint32_t)row << 4) | (uint32_t)(nt * kTile - len);
       sum += nt;
+      is_long |= nt > S::kUnitTiles;
+      is_empty |= !skip && nt == 0;
     }
     int inc = sum;
 #pragma unroll
@@ -194,24 +205,25 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       if (lane >= o) inc += v;
     }
     if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
+    any_long = __syncthreads_or(is_long);
+    int before = inc - sum, all = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int v = wsum[w];
+      before += w < warp ? v : 0;
+      all += v;
+    }
     for (int b = b0; b < b1; ++b) {
       const int nt = pre[b];
       pre[b] = before;
       before += nt;
     }
-    if (tid == 0) {
-      int all = 0;
-      for (int w = 0; w < W; ++w) all += wsum[w];
-      pre[n] = all;
-    }
-    __syncthreads();
+    if (tid == 0) pre[n] = all;
+    any_empty = __syncthreads_or(is_empty);
   }
   const AttnSeqs seqs{pre, meta};
   // rows without a key: zeros, and the logarithm of an empty sum
-  for (int b = blockIdx.x; b < n; b += gridDim.x) {
+  for (int b = blockIdx.x; any_empty && b < n; b += gridDim.x) {
     if (seqs.tiles(b) != 0 || meta[b] == kNoRow) continue;
     const int64_t row = seqs.row(b);
     for (int i = tid; i < p.n_q * (D / 2); i += T) reinterpret_cast<uint32_t*>(p.out + row * p.n_q * D)[i] = 0u;
@@ -219,11 +231,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       for (int i = tid; i < p.n_q; i += T) p.lse[row * p.n_q + i] = kNegInf;
   }
   const long long total = (long long)pre[n] * heads;
-  const int ctas = attn_ctas(total, gridDim.x, W);
   const int cta = blockIdx.x;
-  if (cta >= ctas) return;
-  const AttnLine line(total, ctas);
-  const long long s0 = line.start(cta), s1 = line.start(cta + 1);
+  const bool by_unit = !any_long && n * heads <= (int)gridDim.x;
+  const AttnLine line(total, attn_ctas(total, gridDim.x, W));
+  long long s0, s1;
+  if (!attn_share(seqs, n, heads, p.by_heads, by_unit, line, cta, &s0, &s1)) return;
   const AttnLine part(s1 - s0, W);
   const long long w0 = s0 + part.start(warp), w1 = s0 + part.start(warp + 1);
 
@@ -231,8 +243,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
   if (lane < 2) part_unit[2 * warp + lane] = -1;
 
-  auto put = [&](int64_t row, int i, float v) {            // entry i of the row, in o's order
-    const int at = p.order[i];
+  auto put = [&](int64_t row, int at, float v) {           // an entry at its column in o's order
     if ((unsigned)at < (unsigned)(p.n_q * D)) p.out[row * p.n_q * D + at] = out16(v, p.out_bf16);
     else *p.status = SVQ_ERR_INVALID_ARG;
   };
@@ -244,8 +255,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
     const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
     const int i = head * D + d;
     if (p.order) {
+      int at[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) put(row, i + e, v[e]);
+      for (int e = 0; e < 4; ++e) at[e] = __ldg(p.order + i + e);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) put(row, at[e], v[e]);
     } else {
       const uint2 w = p.out_bf16 ? make_uint2(pack2<true>(v[0], v[1]), pack2<true>(v[2], v[3]))
                                  : make_uint2(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]));
@@ -254,6 +268,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
     if (p.lse && d == 0) p.lse[row * p.n_q + head] = log_sum(ml.x, ml.y);
   };
 
+  // The drained ring takes both parts of its warp.  A part left in mid-range waits
+  // in the workspace until then.
+  static_assert(2 * R * kPitch * 4 <= S::kStages * S::kStage, "two parts in a warp's ring");
+  auto part_room = [&](int w, int slot) {
+    return reinterpret_cast<float*>(smem + (size_t)w * S::kStages * S::kStage) + (slot ? 0 : R * kPitch);
+  };
+  float* spilled = p.warp_part + ((int64_t)cta * W + warp) * R * kPitch;
   const int todo = (int)(w1 - w0);
   if (todo > 0) {
     // ---- this warp's stream of tiles.  Every 32 tiles each lane finds the place of
@@ -472,8 +493,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
         // A part: in mid-range (the ring is in use) to the workspace, else to the
         // ring, which is drained: every tile of the range has been waited for.
         const int slot = range_ends;
-        float* dst = slot ? reinterpret_cast<float*>(smem + (size_t)warp * S::kStages * S::kStage)
-                          : p.warp_part + ((int64_t)cta * W + warp) * R * kPitch;
+        float* dst = slot ? part_room(warp, 1) : spilled;
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
@@ -506,10 +526,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
         if (p.order) {
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
+            int at[4];                                     // all four before the first store
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (r + (e & 1) < count)
-                put(row, (head0 + r + (e & 1)) * D + ks * 16 + g8 + (e >> 1) * 8, o[ks][q][e] * (e & 1 ? i1 : i0));
+              at[e] = r + (e & 1) < count
+                          ? __ldg(p.order + (head0 + r + (e & 1)) * D + ks * 16 + g8 + (e >> 1) * 8) : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (r + (e & 1) < count) put(row, at[e], o[ks][q][e] * (e & 1 ? i1 : i0));
           }
         } else {
           // 8 x 8 transposes turn (entry, two heads) into (head, two entries): 4-byte stores
@@ -531,38 +555,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
     }
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __syncwarp();
+  if (part_unit[2 * warp] >= 0) {
+    const float4* src = reinterpret_cast<const float4*>(spilled);
+    float4* dst = reinterpret_cast<float4*>(part_room(warp, 0));
+#pragma unroll 8
+    for (int i = lane; i < R * kPitch / 4; i += 32) dst[i] = __ldcg(src + i);
+  }
   __syncthreads();
 
   // ---- join the warps' parts.  Parts of one unit are neighbours in the order
-  // (warp, slot).  Thread (x, r) turns the maximum of head r of part x into its
-  // weight among the parts of its unit; the first of them gets the joined maximum
-  // and sum.  No condition stands before a load, so the loads do not queue.
-  static_assert(R * kPitch * 4 + P * R * 4 <= S::kStages * S::kStage, "weights behind the first warp's part");
-  float* part_w = reinterpret_cast<float*>(smem + S::kStages * S::kStage) - P * R;      // [P][R]
-  {
-    const int x = min(tid / R, P - 1), r = tid % R, u = part_unit[x];
-    float2 ml[P];
-    float M = kNegInf, L = 0.f, f = 0.f;
-#pragma unroll
-    for (int y = 0; y < P; ++y) {
-      const int v = part_unit[y];
-      ml[y] = part_ml[y][r];
-      if (v != u || v < 0) ml[y] = make_float2(kNegInf, 0.f);
-      M = fmaxf(M, ml[y].x);
-    }
-#pragma unroll
-    for (int y = 0; y < P; ++y) {
-      const float g = part_weight(ml[y].x, M);
-      L = fmaf(g, ml[y].y, L);
-      if (y == x) f = g;
-    }
-    __syncthreads();
-    if (tid < P * R) {
-      part_w[x * R + r] = f;
-      part_ml[x][r] = make_float2(M, L);
-    }
-    __syncthreads();
-  }
+  // (warp, slot): slots 1 of consecutive warps, then perhaps a slot 0.  A warp
+  // takes a row (or two of 64 entries) of a unit at a time, a lane V times 4
+  // entries; no condition stands before a load, so the loads do not queue.
+  constexpr int V = D == 256 ? 2 : 1, kRows = D == 64 ? 2 : 1;
+  constexpr int kItems = R / kRows;                        // of a unit
+  const int r_sub = D == 64 ? lane >> 4 : 0, d_lane = D == 64 ? (lane & 15) * 4 : lane * 4;    // + 128 for V = 1
   const int my_unit = lane < P ? part_unit[lane] : -1;
   const uint32_t have = __ballot_sync(0xFFFFFFFFu, my_unit >= 0);
   const uint32_t lower = have & ((1u << lane) - 1u);
@@ -570,140 +578,167 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, my_unit >= 0 && (!lower || prev != my_unit));
   // part x of a unit: CTA c0 + x's, in its place 1 if the unit begins there and else in place 0
   auto cta_part = [&](const UnitOut& u, int x) { return p.cta_part + ((u.c0 + x) * 2 + (x == 0)) * kPartWords; };
-  int shared_by[2] = {-1, -1};                             // first parts of the units that other CTAs share
 #pragma unroll 1
-  for (uint32_t left = firsts; left; left &= left - 1) {
+  for (int it = warp; it < __popc(firsts) * kItems; it += W) {
+    uint32_t left = firsts;
+#pragma unroll 1
+    for (int k = it / kItems; k > 0; --k) left &= left - 1;
     const int a = __ffs(left) - 1;
     const uint32_t later = left & (left - 1);              // the next unit's first part
     const uint32_t members = have & ~((1u << a) - 1u) & (later ? (later & (0u - later)) - 1u : ~0u);
+    const int last = 31 - __clz(members), w0p = a >> 1, n_parts = (last >> 1) - w0p + 1;
     const UnitOut u = part_to[a];
-    const int count = u.heads & 255;
-    float* far = nullptr;
-    if (u.c0 != u.c1) {
-      shared_by[u.c0 == cta] = a;
-      far = cta_part(u, cta - u.c0);
-    }
-#pragma unroll 1
-    for (int i = tid * 4; i < count * D; i += T * 4) {
-      const int r = i / D, d = i - r * D;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {                        // the parts in the ring
-        const bool in = (members >> (2 * w + 1)) & 1;
-        float4 v = *reinterpret_cast<const float4*>(smem + (size_t)w * S::kStages * S::kStage + (r * kPitch + d) * 4);
-        v = make_float4(in ? v.x : 0.f, in ? v.y : 0.f, in ? v.z : 0.f, in ? v.w : 0.f);
-        weigh(acc, in ? part_w[(2 * w + 1) * R + r] : 0.f, v);
-      }
-#pragma unroll 1
-      for (uint32_t x = members & 0x55555555u; x; x &= x - 1) {      // those left in mid-range
-        const int y = __ffs(x) - 1;
-        weigh(acc, part_w[y * R + r], __ldcg(reinterpret_cast<const float4*>(
-                                     p.warp_part + ((int64_t)cta * W + (y >> 1)) * R * kPitch + r * kPitch + d)));
-      }
-      const float2 ml = part_ml[a][r];
-      if (far) {
-        *reinterpret_cast<float4*>(far + i) = acc;
-        if (d == 0) *reinterpret_cast<float2*>(far + R * D + 2 * r) = ml;
-      } else {
-        put4(u.row, (u.heads >> 8) + r, d, ml, acc);
-      }
-    }
-  }
-  if (shared_by[0] < 0 && shared_by[1] < 0) return;
-
-  // ---- join the CTAs' parts: the last of the unit's CTAs to get here adds them.
-  __syncthreads();
-  if (tid < 2) {
-    const int a = tid ? shared_by[1] : shared_by[0];
-    bool last = false;
-    if (a >= 0) {
-      // Release of this CTA's parts (the barrier above puts them before it) and
-      // acquire of the others'; wraps to zero with the last arrival.
-      const unsigned others = (unsigned)(part_to[a].c1 - part_to[a].c0);
-      unsigned old;
-      asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
-                   : "=r"(old)
-                   : "l"(p.counters + part_to[a].c0), "r"(others)
-                   : "memory");
-      last = old == others;
-    }
-    joined[tid] = last;
-  }
-  __syncthreads();
-#pragma unroll 1
-  for (int s = 0; s < 2; ++s) {
-    if (!joined[s]) continue;
-    const UnitOut u = part_to[s ? shared_by[1] : shared_by[0]];
-    const int parts = u.c1 - u.c0 + 1, count = u.heads & 255;
-    // Shared memory: the parts' weights, the joined (maximum, sum) of each head,
-    // then as many parts' entries as fit, copied there all at once.
-    float2* ml = reinterpret_cast<float2*>(smem);          // [parts][R], then [R] joined
-    float2* top = ml + parts * R;
-    float* hold = reinterpret_cast<float*>(top + R);
-    constexpr int kPieces = (R * D + 4 * T - 1) / (4 * T);
-    float4 acc[kPieces];
-#pragma unroll
-    for (int k = 0; k < kPieces; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int words = count * D, fit = (S::kRing - (parts + 1) * R * 8) / (words * 4);
-    for (int first = 0; first < parts; first += fit) {
-      const int now = min(fit, parts - first);
-      const uint32_t hold_at = sm100::smem_u32(hold);
-#pragma unroll 1
-      for (int i = tid * 4; i < words; i += T * 4) {
-#pragma unroll 8
-        for (int x = 0; x < now; ++x) cp_async16(hold_at + (x * words + i) * 4, cta_part(u, first + x) + i, 16);
-      }
-      cp_commit();
-      if (first == 0) {
+    const int r = it % kItems * kRows + r_sub;
+    if (it % kItems * kRows >= (u.heads & 255)) continue;
+    // part x is slot 1 of warp w0p + x, but for the last, which is `last`
+    float M = kNegInf, L = 0.f;
 #pragma unroll 4
-        for (int i = tid; i < parts * R; i += T)
-          ml[i] = __ldcg(reinterpret_cast<const float2*>(cta_part(u, i / R) + R * D) + i % R);
-        __syncthreads();
-        if (tid < R) {
-          float M = kNegInf, L = 0.f;
-#pragma unroll 8
-          for (int x = 0; x < parts; ++x) M = fmaxf(M, ml[x * R + tid].x);
-#pragma unroll 8
-          for (int x = 0; x < parts; ++x) {
-            const float2 v = ml[x * R + tid];
-            const float f = part_weight(v.x, M);
-            ml[x * R + tid].x = f;
-            L = fmaf(f, v.y, L);
+    for (int x = 0; x < n_parts; ++x) M = fmaxf(M, part_ml[min(2 * (w0p + x) + 1, last)][r].x);
+    float4 acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = 0; x < n_parts; ++x) {
+      const int y = min(2 * (w0p + x) + 1, last);
+      const float2 ml = part_ml[y][r];
+      const float f = part_weight(ml.x, M);
+      L = fmaf(f, ml.y, L);
+      const float* src = part_room(y >> 1, y & 1) + r * kPitch + d_lane;
+#pragma unroll
+      for (int k = 0; k < V; ++k) weigh(acc[k], f, reinterpret_cast<const float4*>(src)[k * 32]);
+    }
+    if (r >= (u.heads & 255)) continue;
+    if (u.c0 != u.c1) {
+      float* far = cta_part(u, cta - u.c0);
+#pragma unroll
+      for (int k = 0; k < V; ++k) reinterpret_cast<float4*>(far + r * D + d_lane)[k * 32] = acc[k];
+      if (d_lane == 0) *reinterpret_cast<float2*>(far + R * D + 2 * r) = make_float2(M, L);
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) put4(u.row, (u.heads >> 8) + r, d_lane + k * 128, make_float2(M, L), acc[k]);
+    }
+  }
+  // The CTA's first unit may have begun in another CTA, its last may go on in one.
+  if (!firsts) return;
+  const int a0 = __ffs(firsts) - 1, a1 = 31 - __clz(firsts);
+  const bool from_before = part_to[a0].c0 < cta, goes_on = part_to[a1].c0 == cta && part_to[a1].c1 > cta;
+  if (!from_before && !goes_on) return;
+
+  // ---- join the CTAs' parts, up to kFan neighbours at a time: the last of them to
+  // get here adds them and goes on in their place (a wide unit on many CTAs would
+  // keep a single one busy for longer than the whole loop).
+  auto arrive = [&](const UnitOut& u, int stride, int level) {
+    int members;
+    const int first = attn_group(u.c1 - u.c0 + 1, kFan, stride, cta - u.c0, &members);
+    if (members == 1) return true;
+    // Release of this CTA's part (a barrier puts all threads' stores before it)
+    // and acquire of the others'; the counter wraps to zero with the last.
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+                 : "=r"(old)
+                 : "l"(p.counters + level * (int)gridDim.x + u.c0 + first), "r"((unsigned)(members - 1))
+                 : "memory");
+    return old == (unsigned)(members - 1);
+  };
+  constexpr int kLanes = 32 / kRows;                       // lanes of a row: lane x looks at part x
+  static_assert(kFan <= kLanes, "a lane for each part of a group");
+#pragma unroll 1
+  for (int stride = 1, level = 0;; stride *= kFan, ++level) {
+    __syncthreads();                                       // the parts of this CTA are written
+    if (tid < 2) {
+      const bool mine = level == 0 ? (tid ? goes_on : from_before) : joined[tid];
+      joined[tid] = mine && arrive(part_to[tid ? a1 : a0], stride, level);
+    }
+    __syncthreads();
+    if (!joined[0] && !joined[1]) return;
+#pragma unroll 1
+    for (int it = warp; it < 2 * kItems; it += W) {
+      const int s = it / kItems;
+      if (!joined[s]) continue;
+      const UnitOut u = part_to[s ? a1 : a0];
+      const int r = it % kItems * kRows + r_sub;
+      if (it % kItems * kRows >= (u.heads & 255)) continue;
+      int members;
+      const int first = attn_group(u.c1 - u.c0 + 1, kFan, stride, cta - u.c0, &members);
+      const float* base = cta_part(u, first);
+      // parts beyond the first stand 2 * stride places apart, in place 0
+      const float* rest = cta_part(u, first + stride);
+      const int64_t pitch = (int64_t)stride * 2 * kPartWords;
+      auto part_at = [&](int x) { return x == 0 ? base : rest + (x - 1) * pitch; };
+      const int mine = min(lane % kLanes, members - 1);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_at(mine) + R * D + 2 * r));
+      constexpr int kBatch = 8;
+      float4 v[kBatch][V];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)                     // beyond the last: loaded again, without weight
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+          v[x][k] = __ldcg(reinterpret_cast<const float4*>(part_at(min(x, members - 1)) + r * D + d_lane) + k * 32);
+      float M = lane % kLanes < members ? ml.x : kNegInf;
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+      const float f = lane % kLanes < members ? part_weight(ml.x, M) : 0.f;
+      float L = f == 0.f ? 0.f : f * ml.y;
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
+      float4 acc[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int x0 = 0;; x0 += kBatch) {
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const float g = __shfl_sync(0xFFFFFFFFu, f, x0 + x, kLanes);
+          const bool in = x0 + x < members;
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            const float4 t = v[x][k];
+            weigh(acc[k], g, make_float4(in ? t.x : 0.f, in ? t.y : 0.f, in ? t.z : 0.f, in ? t.w : 0.f));
           }
-          top[tid] = make_float2(M, L);
         }
-      }
-      cp_wait<0>();
-      __syncthreads();
+        if (x0 + kBatch >= members) break;
 #pragma unroll
-      for (int k = 0; k < kPieces; ++k) {
-        const int i = (tid + k * T) * 4;
-        if (i >= words) break;
-#pragma unroll 8
-        for (int x = 0; x < now; ++x)
-          weigh(acc[k], ml[(first + x) * R + i / D].x, *reinterpret_cast<const float4*>(hold + x * words + i));
-      }
-      __syncthreads();                                     // before the next round's copies
-    }
+        for (int x = 0; x < kBatch; ++x)
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-      const int i = (tid + k * T) * 4;
-      if (i < words) put4(u.row, (u.heads >> 8) + i / D, i % D, top[i / D], acc[k]);
+          for (int k = 0; k < V; ++k)
+            v[x][k] = __ldcg(
+                reinterpret_cast<const float4*>(part_at(min(x0 + kBatch + x, members - 1)) + r * D + d_lane) + k * 32);
+      }
+      if (r >= (u.heads & 255)) continue;
+      if (stride * kFan > u.c1 - u.c0) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) put4(u.row, (u.heads >> 8) + r, d_lane + k * 128, make_float2(M, L), acc[k]);
+      } else {
+        float* far = const_cast<float*>(base);
+#pragma unroll
+        for (int k = 0; k < V; ++k) reinterpret_cast<float4*>(far + r * D + d_lane)[k * 32] = acc[k];
+        if (d_lane == 0) *reinterpret_cast<float2*>(far + R * D + 2 * r) = make_float2(M, L);
+      }
     }
-    __syncthreads();                                       // before shared memory is used for the other unit
+    __syncthreads();
+    if (tid < 2 && joined[tid]) {
+      const UnitOut u = part_to[tid ? a1 : a0];
+      joined[tid] = stride * kFan <= u.c1 - u.c0;          // not yet the whole unit
+    }
+    __syncthreads();
+    if (!joined[0] && !joined[1]) return;
   }
 }
 
 template <int D>
+constexpr size_t smem_bytes(int n_seqs) { return Shape<D>::kRing + (size_t)(2 * n_seqs + 1) * 4; }
+
+template <int D>
 void plan_d(int n_seqs, PagedAttnPlan* plan) {
   plan->warps = Shape<D>::kWarps;
-  plan->smem = Shape<D>::kRing + (size_t)(2 * n_seqs + 1) * 4;
+  plan->smem = smem_bytes<D>(n_seqs);
 }
 
 template <int D, int NQ, bool BF16>
 cudaError_t launch_dq(const PagedAttnParams& p, const PagedAttnPlan& plan, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, NQ, BF16>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan.smem);
+  // the most any call needs, so that concurrent first calls agree
+  static std::atomic<int> have[64];
+  const cudaError_t e = allow_smem(paged_attn_kernel<D, NQ, BF16>, smem_bytes<D>(kMaxSeqs), have);
   if (e != cudaSuccess) return e;
   return launch_dependent(paged_attn_kernel<D, NQ, BF16>, (unsigned)plan.ctas, Shape<D>::kThreads, plan.smem, 1, st,
                           p);

@@ -17,6 +17,7 @@ import pytest
 from bit_spherical_vector_b200 import build as svq_build
 
 HARNESS = r"""
+#include <algorithm>
 #include <cstdio>
 #include <map>
 #include <random>
@@ -24,7 +25,7 @@ HARNESS = r"""
 #include <vector>
 #include "attn_split.cuh"
 using namespace svq;
-static long long bad = 0, cases = 0, split_units = 0;
+static long long bad = 0, cases = 0, split_units = 0, units = 0;
 #define CHECK(c, ...) do { if (!(c)) { if (++bad < 20) { printf(__VA_ARGS__); printf("\n"); } } } while (0)
 
 static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
@@ -39,18 +40,21 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
   const AttnSeqs s{pre.data(), meta.data()};
   for (int b = 0; b < n; ++b) CHECK(s.len(b) == lens[b] && s.row(b) == b, "meta %d", b);
   const long long total = (long long)pre[n] * heads;
-  const int ctas = attn_ctas(total, grid, W);
-  CHECK(total > 0 || ctas == 0, "empty call has CTAs");
-  ++cases;
-  const AttnLine line(total, ctas > 0 ? ctas : 1);
+  const AttnLine line(total, attn_ctas(total, grid, W));
   const FastDiv by_heads(heads);
+  int longest = 0;
+  for (int b = 0; b < n; ++b) longest = std::max(longest, s.tiles(b));
+  const bool by_unit = longest <= 4 * W && (long long)n * heads <= grid;
+  ++cases;
+  units += by_unit;
   std::map<long long, int> written;                       // unit -> times written
   std::map<int, std::pair<long long, int>> counter;       // counter -> unit, arrivals
   std::map<long long, std::set<int>> far;                 // unit -> CTAs that left a part
   long long expect_b = 0, expect_h = 0, expect_t = -1;    // the line in order
   int eb = -1;
-  for (int c = 0; c < ctas; ++c) {
-    const long long s0 = line.start(c), s1 = line.start(c + 1);
+  for (int c = 0; c < grid; ++c) {
+    long long s0, s1;
+    if (!attn_share(s, n, heads, by_heads, by_unit, line, c, &s0, &s1)) continue;
     const AttnLine share(s1 - s0, W);
     CHECK(s1 > s0, "empty CTA");
     std::vector<long long> part(2 * W, -1);
@@ -97,6 +101,17 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
       const long long unit = part[a];
       int e = a + 1;
       while (e < 2 * W && (part[e] < 0 || part[e] == unit)) ++e;
+      // the kernel counts a unit's parts as slots 1 of consecutive warps and perhaps a last slot 0
+      int last = e - 1, at = a;
+      while (part[last] < 0) --last;
+      for (int x = 0; x < last / 2 - a / 2 + 1; ++x) {
+        const int y = std::min(2 * (a / 2 + x) + 1, last);
+        while (at < e && part[at] < 0) ++at;
+        CHECK(y == at, "part %d of unit %lld", x, unit);
+        ++at;
+      }
+      while (at < e && part[at] < 0) ++at;
+      CHECK(at == e, "parts of unit %lld left over", unit);
       const int b = (int)(unit / heads), h = (int)(unit % heads);
       const long long u0 = (long long)pre[b] * heads + (long long)h * s.tiles(b), u1 = u0 + s.tiles(b);
       if (u0 >= s0 && u1 <= s1) written[unit]++;
@@ -105,18 +120,56 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
         CHECK(!used[slot], "workspace slot twice");
         used[slot] = true;
         const int c0 = line.range_of(u0), c1 = line.range_of(u1 - 1);
-        CHECK(c0 <= c && c <= c1 && c1 > c0, "CTAs of a unit");
+        CHECK(!by_unit && c0 <= c && c <= c1 && c1 > c0, "CTAs of a unit");
         CHECK((slot == 1) == (c == c0), "slot of the first CTA");
         CHECK(far[unit].insert(c).second, "two parts of a unit in one CTA");
         auto& k = counter[c0];
         if (k.second == 0) k.first = unit;
         CHECK(k.first == unit, "counter shared");
-        if (++k.second == c1 - c0 + 1) written[unit]++;
+        if (++k.second == c1 - c0 + 1) written[unit]++;      // joined below, level by level
       }
       a = e;
     }
   }
   split_units += (long long)far.size();
+  // The joins: CTAs arrive in random order, the last of a group adds its parts and goes on for them.
+  static std::mt19937 shuffle(11);
+  for (int fan : {8, 16, 128}) {
+    std::map<std::pair<int, int>, std::pair<long long, int>> at;       // (level, counter) -> unit, arrivals
+    for (auto& f : far) {
+      const int c0 = *f.second.begin(), n = (int)f.second.size();
+      CHECK(*f.second.rbegin() == c0 + n - 1, "CTAs of a unit are neighbours");
+      std::vector<int> order(f.second.begin(), f.second.end());
+      std::shuffle(order.begin(), order.end(), shuffle);
+      std::vector<std::set<int>> holds(n);                  // parts summed in each place
+      for (int i = 0; i < n; ++i) holds[i] = {i};
+      int done = 0;
+      for (int c : order) {
+        for (int stride = 1, level = 0;; stride *= fan, ++level) {
+          CHECK(level < 3, "levels");
+          int m;
+          const int first = attn_group(n, fan, stride, c - c0, &m);
+          if (m > 1) {
+            auto& k = at[{level, c0 + first}];
+            if (k.second == 0) k.first = f.first;
+            CHECK(k.first == f.first, "counter shared on a level");
+            if (++k.second < m) break;
+          }
+          for (int x = 1; x < m; ++x) {
+            CHECK(first + x * stride < n, "beyond the unit");
+            for (int v : holds[first + x * stride]) CHECK(holds[first].insert(v).second, "added twice");
+            holds[first + x * stride].clear();
+          }
+          if (stride * fan > n - 1) {
+            ++done;
+            CHECK(first == 0 && (int)holds[0].size() == n, "all parts in the sum");
+            break;
+          }
+        }
+      }
+      CHECK(done == 1, "joined %d times", done);
+    }
+  }
   for (auto& k : counter)
     CHECK((int)far[k.second.first].size() == k.second.second, "arrivals");
   for (int b = 0; b < n; ++b)
@@ -157,7 +210,7 @@ int main() {
     for (long long x : {(long long)k * d - 1, (long long)k * d, (long long)k * d + d - 1, (long long)(r() >> 1), 0x7FFFFFFFll, 0ll})
       if (x >= 0 && x <= 0x7FFFFFFF) CHECK(f.div((int)x) == x / d, "%lld / %d", x, d);
   }
-  printf("cases=%lld split=%lld bad=%lld\n", cases, split_units, bad);
+  printf("cases=%lld split=%lld units=%lld bad=%lld\n", cases, split_units, units, bad);
   return bad ? 1 : 0;
 }
 """
@@ -177,4 +230,4 @@ def test_every_tile_once_and_every_unit_written_once(tmp_path):
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout
     counts = dict(kv.split("=") for kv in r.stdout.split())
-    assert int(counts["cases"]) > 400 and int(counts["split"]) > 1000
+    assert int(counts["cases"]) > 400 and int(counts["split"]) > 1000 and int(counts["units"]) > 20
