@@ -55,6 +55,9 @@ struct RopeCacheParams {
   KvView kv;
   float eps, factor;
   int M, n_q, rot, interleaved;
+  // set by the launcher: slices of a row, of its queries, of its keys; steps of a slice
+  FastDiv by_slices;
+  int q_slices, kv_slices, steps;
 };
 // x_dtype: 0 fp32, 1 fp16, 2 bf16; kv_bf16: type of q_out and the cache.
 cudaError_t launch_rope_cache(const RopeCacheParams& p, int head_dim, int x_dtype, int kv_bf16, int num_sms,
@@ -105,10 +108,10 @@ cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<int> (&have)[64]) {
 // Launch with programmatic stream serialization (the kernel waits with
 // griddepcontrol.wait) and, for cluster > 1, as clusters of that many CTAs.
 template <typename Kern, typename P>
-cudaError_t launch_dependent(Kern kern, unsigned grid, unsigned threads, size_t smem, unsigned cluster,
+cudaError_t launch_dependent(Kern kern, dim3 grid, unsigned threads, size_t smem, unsigned cluster,
                              cudaStream_t st, const P& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -12,11 +12,14 @@
 // whole turns are dropped there, and only the remaining half turn goes to fp32
 // (sincospi): off by 2e-7 at any position an int32 holds up to 10^8.
 //
-// One read of q|k|v and one write of q, k and v bounds it.  A warp takes U
-// consecutive heads of one row, a lane D / 32 consecutive entries of each: rows
-// are read and written whole, the norm is a butterfly, the partner of a
-// half-split pair is one shuffle away (rot / 2 is a multiple of D / 32), and the
-// sines of a row are formed once for the U heads.
+// One read of q|k|v and one write of q, k and v bounds long calls in principle,
+// latency short ones.  A warp takes heads of one kind (queries, keys or values) of
+// one row.  A head is spread over D / 8 lanes, each with two chunks of 4 entries
+// that lie half the rotated part apart (or half the rest of the head), so both
+// entries of a half-split pair are in one lane, as those of a neighbour pair are.
+// The sines are formed once for the warp's heads, a share by each of the 256 / D
+// lanes that need the same ones, and multiplied with gamma.  Nothing else is
+// exchanged but the sum of squares, and warps do not wait for one another.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,179 +37,209 @@ __device__ __forceinline__ float to_f32(uint16_t v) {
   return BF16 ? __bfloat162float(__ushort_as_bfloat16(v)) : __half2float(__ushort_as_half(v));
 }
 template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if (BF16)
-    return (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(a)) |
-           ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(b)) << 16);
-  return (uint32_t)__half_as_ushort(__float2half_rn(a)) | ((uint32_t)__half_as_ushort(__float2half_rn(b)) << 16);
+__device__ __forceinline__ uint32_t pack2(float a, float b) {      // a in the low half
+  if (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// E consecutive 32-bit words (E = 1, 2 or 4 per vector access).
-template <int N>
-__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[N]) {
-  if constexpr (N == 1) {
-    w[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if constexpr (N == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x; w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i / 4];
-      w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+// Four entries of type XT (0 fp32, 1 fp16, 2 bf16) as they are stored.
+template <int XT>
+struct Chunk {
+  uint32_t w[XT == 0 ? 4 : 2];
+  static constexpr int kSize = XT == 0 ? 4 : 2;            // bytes of an entry
+  __device__ void load(const void* p) {
+    if constexpr (XT == 0) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x; w[1] = v.y;
     }
   }
-}
-template <int N>
-__device__ __forceinline__ void store_words(void* p, const uint32_t (&w)[N]) {
-  if constexpr (N == 1) *reinterpret_cast<uint32_t*>(p) = w[0];
-  else if constexpr (N == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+  __device__ float get(int i) const {
+    if constexpr (XT == 0) return __uint_as_float(w[i]);
+    else return to_f32<XT == 2>((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+  }
+};
 
-// XT: type of q|k|v (0 fp32, 1 fp16, 2 bf16); BF16: type of the cache and q_out.
-template <int D, int XT, bool BF16, int U>
+// BF16: type of the cache and q_out; IL: neighbour pairs.  A step is 256 / D heads;
+// a warp takes p.steps of them, U at a time with the next U on their way (U = 1:
+// one step, and no loop).
+template <int D, int XT, bool BF16, bool IL, int U>
 __global__ void __launch_bounds__(kThreads) rope_cache_kernel(const __grid_constant__ RopeCacheParams p) {
-  constexpr int E = D / 32;                        // entries per lane
-  constexpr int XW = XT == 0 ? E : E / 2;          // 32-bit words per lane and head, read
-  const int lane = threadIdx.x & 31;
-  const int n_kv = p.kv.n_heads, roped = p.n_q + n_kv, heads = roped + n_kv;
-  const int chunks = (heads + U - 1) / U;
-  const long long wid = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int m = (int)(wid / chunks), h0 = (int)(wid - (long long)m * chunks) * U;
-  const int j0 = lane * E;
-  const int half = p.rot >> 1;
-  const bool turned = j0 < p.rot;
+  constexpr int kLanes = D / 8, kHeads = 32 / kLanes;      // lanes of a head, heads of a step
+  const int lane = threadIdx.x & 31, n_kv = p.kv.n_heads;
+  // the warp's row and slice of its heads; kind: 0 queries, 1 keys, 2 values
+  const int wid = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int m = p.by_slices.div(wid), y = wid - m * (int)p.by_slices.d;
+  if (m >= p.M) return;
+  const int kind = y < p.q_slices ? 0 : y < p.q_slices + p.kv_slices ? 1 : 2;
+  const int heads = kind == 0 ? p.n_q : n_kv;
+  const int first = (y - (kind == 0 ? 0 : kind == 1 ? p.q_slices : p.q_slices + p.kv_slices)) * p.steps * kHeads;
+  const uint16_t* gamma = kind == 0 ? p.q_gamma : kind == 1 ? p.k_gamma : nullptr;
+  const int half = p.rot >> 1, i = lane % kLanes;
+  // the lane's chunks: entries c0.. and c1.. of its heads
+  const bool turned = i * 8 < p.rot;
+  const int c0 = turned ? i * 4 : p.rot + (i * 4 - half);
+  const int c1 = c0 + (turned ? half : (D - p.rot) >> 1);
+  // its pairs e = 0..3: (c0 + e, c1 + e) if half split, else two neighbour pairs in each chunk
+  auto pair_of = [&](int e) { return IL ? ((e & 2 ? c1 : c0) >> 1) + (e & 1) : c0 + e; };
 
   // weights and constants, before the previous kernel has finished
-  double freq[E];
-  if (turned && h0 < roped) {
+  constexpr int kShare = 4 / kHeads;                       // pairs whose sines this lane forms
+  const int e0 = lane / kLanes * kShare;
+  double freq[kShare];
+  Chunk<1> g0, g1;
+  if (kind < 2) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int j = j0 + e;
-      const int i = p.interleaved ? (j >> 1) : (j < half ? j : j - half);
-      freq[e] = __ldg(p.inv_freq + i) * 0.15915494309189533577;        // 1 / (2 pi): turns per position
-    }
+    for (int e = 0; e < kShare; ++e)                       // turns per position
+      freq[e] = turned ? __ldg(p.inv_freq + pair_of(e0 + e)) * 0.15915494309189533577 : 0.0;
+  }
+  if (gamma) {
+    g0.load(gamma + c0);
+    g1.load(gamma + c1);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (m >= p.M) return;
-  const int slot = p.slots[m];
-  if (slot < 0) return;                            // a padding row: nothing of it is read or written
+  const int slot = p.slots[m], position = p.positions[m];
+  const int h0 = first + lane / kLanes;                    // the lane's heads: h0, h0 + kHeads, ..
+  // both read and write pointer walk from step to step
+  const char* src = reinterpret_cast<const char*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+                    (m * (kind == 0 ? p.ldq : kind == 1 ? p.ldk : p.ldv) + h0 * D + c0) * Chunk<XT>::kSize;
+  const int src_c1 = (c1 - c0) * Chunk<XT>::kSize;
+  const int my_steps = min(p.steps, (heads - h0 + kHeads - 1) / kHeads);     // with a head for this lane
+  using Batch = Chunk<XT>[U][2];
+  auto load = [&](Batch& x, int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s + u < my_steps) {
+        x[u][0].load(src);
+        x[u][1].load(src + src_c1);
+      }
+      src += kHeads * D * Chunk<XT>::kSize;
+    }
+  };
+  Batch xa, xb;
+  load(xa, 0);
+  if (slot < 0) return;                                    // a padding row
   const int page = slot / p.kv.page_size;
   if (page >= p.kv.n_pages) {
     if (lane == 0) *p.status = SVQ_ERR_INVALID_ARG;
     return;
   }
-
-  uint32_t raw[U][XW];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u;
-    if (h < heads) {
-      const char* x = reinterpret_cast<const char*>(h < p.n_q ? p.q : h < roped ? p.k : p.v);
-      const int64_t ld = h < p.n_q ? p.ldq : h < roped ? p.ldk : p.ldv;
-      const int hh = h < p.n_q ? h : h < roped ? h - p.n_q : h - roped;
-      load_words<XW>(x + (m * ld + (int64_t)hh * D + j0) * (XT == 0 ? 4 : 2), raw[u]);
-    }
-  }
-
-  float c[E], s[E];                                // s carries the sign of the partner's term
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    c[e] = 1.f;
-    s[e] = 0.f;
-  }
-  if (turned && h0 < roped) {
-    const double pos = (double)p.positions[m];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int j = j0 + e;
-      if (p.interleaved && (e & 1)) {              // the same angle as the entry before
-        c[e] = c[e - 1];
-        s[e] = -s[e - 1];
-      } else {
-        const double t = pos * freq[e];
-        const float f = (float)(t - rint(t));      // turns in [-1/2, 1/2]
-        float sn, cs;
-        sincospif(2.f * f, &sn, &cs);
-        c[e] = cs * p.factor;
-        s[e] = (p.interleaved || j < half ? -sn : sn) * p.factor;
-      }
-    }
-  }
-  const int mate = j0 < half ? lane + half / E : lane - half / E;     // lane of the half-split partner
   const int64_t at = (int64_t)page * p.kv.page_stride + (int64_t)(slot - page * p.kv.page_size) * p.kv.token_stride;
+  const int64_t head_step = kind == 0 ? D : p.kv.head_stride, step = kHeads * head_step;
+  const int steps = min(p.steps, (heads - first + kHeads - 1) / kHeads);     // of the warp
+  uint16_t* dst = (kind == 0 ? p.q_out + (int64_t)m * p.n_q * D : (kind == 1 ? p.kv.k : p.kv.v) + at) + h0 * head_step + c0;
 
+  // (u, w) -> (u a - w b, u c + w d): the rotation times gamma, for the lane's pairs
+  float ra[4], rb[4], rc[4], rd[4];
+  if (kind < 2) {
+    float cs[kShare], sn[kShare];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int h = h0 + u;
-    if (h >= heads) break;
-    float v[E];
-#pragma unroll
-    for (int w = 0; w < XW; ++w) {
-      if constexpr (XT == 0) {
-        v[w] = __uint_as_float(raw[u][w]);
-      } else {
-        v[2 * w] = to_f32<XT == 2>((uint16_t)(raw[u][w] & 0xFFFFu));
-        v[2 * w + 1] = to_f32<XT == 2>((uint16_t)(raw[u][w] >> 16));
-      }
+    for (int e = 0; e < kShare; ++e) {
+      const double t = (double)position * freq[e];
+      const float f = (float)(t - rint(t));                // turns in [-1/2, 1/2]
+      sincospif(2.f * f, &sn[e], &cs[e]);
+      cs[e] = turned ? cs[e] * p.factor : 1.f;
+      sn[e] *= p.factor;
     }
-    if (h < roped) {
-      const uint16_t* gamma = h < p.n_q ? p.q_gamma : p.k_gamma;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float c = __shfl_sync(0xFFFFFFFFu, cs[e % kShare], i + e / kShare * kLanes);
+      const float s = __shfl_sync(0xFFFFFFFFu, sn[e % kShare], i + e / kShare * kLanes);
+      float gu = 1.f, gw = 1.f;
       if (gamma) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(v[e], v[e], ss);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-        uint32_t g[E / 2];
-        load_words<E / 2>(gamma + j0, g);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = v[e] * inv * to_f32<false>((uint16_t)(g[e / 2] >> (16 * (e & 1))));
+        gu = IL ? (e & 2 ? g1 : g0).get((e & 1) * 2) : g0.get(e);
+        gw = IL ? (e & 2 ? g1 : g0).get((e & 1) * 2 + 1) : g1.get(e);
       }
-      if (p.interleaved) {
+      ra[e] = gu * c;
+      rb[e] = gw * s;
+      rc[e] = gu * s;
+      rd[e] = gw * c;
+    }
+  }
+
+  auto compute = [&](const Batch& x, int s) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (s + u >= steps) break;
+      float v[2][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[0][e] = x[u][0].get(e);
+        v[1][e] = x[u][1].get(e);
+      }
+      if (kind < 2) {
+        float inv = 1.f;
+        if (gamma) {
+          float ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ss = fmaf(v[0][e], v[0][e], fmaf(v[1][e], v[1][e], ss));
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+          inv = __frsqrt_rn(ss * (1.0f / D) + p.eps);
+        }
         if (turned) {
 #pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            const float a = v[e], b = v[e + 1];
-            v[e] = fmaf(b, s[e], a * c[e]);
-            v[e + 1] = fmaf(a, s[e + 1], b * c[e + 1]);
+          for (int e = 0; e < 4; ++e) {
+            float& a = IL ? v[e >> 1][(e & 1) * 2] : v[0][e];
+            float& b = IL ? v[e >> 1][(e & 1) * 2 + 1] : v[1][e];
+            const float t = fmaf(a, ra[e], -(b * rb[e])) * inv;
+            b = fmaf(a, rc[e], b * rd[e]) * inv;
+            a = t;
+          }
+        } else {                                           // gamma alone: an infinity beside it stays where it is
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            (IL ? v[e >> 1][(e & 1) * 2] : v[0][e]) *= ra[e] * inv;
+            (IL ? v[e >> 1][(e & 1) * 2 + 1] : v[1][e]) *= rd[e] * inv;
           }
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float b = __shfl_sync(0xFFFFFFFFu, v[e], turned ? mate : lane);
-          if (turned) v[e] = fmaf(b, s[e], v[e] * c[e]);
-        }
       }
+      if (s + u < my_steps) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(v[0][0], v[0][1]), pack2<BF16>(v[0][2], v[0][3]));
+        *reinterpret_cast<uint2*>(dst + (c1 - c0)) = make_uint2(pack2<BF16>(v[1][0], v[1][1]), pack2<BF16>(v[1][2], v[1][3]));
+      }
+      dst += step;
     }
-    uint32_t o[E / 2];
-#pragma unroll
-    for (int e = 0; e < E; e += 2) o[e / 2] = pack2<BF16>(v[e], v[e + 1]);
-    uint16_t* dst;
-    if (h < p.n_q) dst = p.q_out + ((int64_t)m * p.n_q + h) * D;
-    else if (h < roped) dst = p.kv.k + at + (int64_t)(h - p.n_q) * p.kv.head_stride;
-    else dst = p.kv.v + at + (int64_t)(h - roped) * p.kv.head_stride;
-    store_words<E / 2>(dst + j0, o);
+  };
+  if constexpr (U == 1) {
+    compute(xa, 0);
+  } else {
+#pragma unroll 1
+    for (int s = 0; s < steps; s += 2 * U) {
+      load(xb, s + U);
+      compute(xa, s);
+      load(xa, s + 2 * U);
+      compute(xb, s + U);
+    }
   }
 }
 
 template <int D, int XT, bool BF16>
-cudaError_t launch_dx(const RopeCacheParams& p, int num_sms, cudaStream_t st) {
-  const long long heads = p.n_q + 2LL * p.kv.n_heads;
-  // One head per warp while that leaves the SMs short of warps, else eight (the
-  // sines of a row are then formed once for eight heads).
-  if (p.M * heads <= (long long)num_sms * 64) {
-    const long long warps = p.M * heads;
-    return launch_dependent(rope_cache_kernel<D, XT, BF16, 1>, (unsigned)((warps + kWarps - 1) / kWarps), kThreads, 0,
-                            1, st, p);
-  }
-  const long long warps = p.M * ((heads + 7) / 8);
-  return launch_dependent(rope_cache_kernel<D, XT, BF16, 8>, (unsigned)((warps + kWarps - 1) / kWarps), kThreads, 0, 1,
-                          st, p);
+cudaError_t launch_dx(RopeCacheParams p, int num_sms, cudaStream_t st) {
+  // Few rows: a step per warp, so that latency is all there is.  Many: as many
+  // steps as leave 48 warps for each SM, at most 16 (the sines of a row are formed
+  // anew in every warp).
+  constexpr int kHeads = 256 / D;
+  const int q_steps = (p.n_q + kHeads - 1) / kHeads, kv_steps = (p.kv.n_heads + kHeads - 1) / kHeads;
+  const long long all = (long long)p.M * (q_steps + 2 * kv_steps), warps = (long long)num_sms * 48;
+  const long long steps = (all + warps - 1) / warps;
+  p.steps = steps < 16 ? (int)steps : 16;
+  p.q_slices = (q_steps + p.steps - 1) / p.steps;
+  p.kv_slices = (kv_steps + p.steps - 1) / p.steps;
+  p.steps = max((q_steps + p.q_slices - 1) / p.q_slices, (kv_steps + p.kv_slices - 1) / p.kv_slices);
+  const int slices = p.q_slices + 2 * p.kv_slices;
+  p.by_slices = FastDiv(slices);
+  const unsigned ctas = (unsigned)(((long long)p.M * slices + kWarps - 1) / kWarps);
+  const auto kern = p.interleaved ? (p.steps == 1 ? rope_cache_kernel<D, XT, BF16, true, 1> : rope_cache_kernel<D, XT, BF16, true, 2>)
+                                  : (p.steps == 1 ? rope_cache_kernel<D, XT, BF16, false, 1> : rope_cache_kernel<D, XT, BF16, false, 2>);
+  return launch_dependent(kern, dim3(ctas), kThreads, 0, 1, st, p);
 }
 
 template <int D>

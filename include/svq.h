@@ -441,7 +441,7 @@ SVQ_API int svq_rope_frequencies(int rot_dim, double base, int scaling, double s
  *   (u, w) -> factor * (u cos a - w sin a, u sin a + w cos a),  a = positions[m] * inv_freq[i]
  * rounded once to the cache's type.  Rotated queries go to q_out
  * [M][n_q_heads][head_dim], keys and (unchanged) values to their slot slots[m].
- * Rows with a negative slot are padding: nothing of them is read or written.  A
+ * Rows with a negative slot are padding: nothing of them is written.  A
  * slot beyond the cache is skipped and sets the device status word.  The rows'
  * slots must be distinct (of two rows with one slot either may win, entry by entry).
  * q [M][n_q_heads * head_dim], k and v [M][n_heads * head_dim] of x_dtype (SVQ_F32,
