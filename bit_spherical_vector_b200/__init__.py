@@ -375,8 +375,15 @@ def _opt(t):
 def _arrays(what: str, dtype, dev: int, *tensors):
     """Contiguous arrays of one type on the current device (None: an optional one that is absent)."""
     for t in tensors:
-        if t is not None and not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
             raise ValueError(f"{what}: an array of {dtype} must be contiguous and on the current CUDA device")
+
+
+def _here(stream):
+    """The current device and the handle of the stream to use there."""
+    import torch
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 class KvCache:
@@ -434,7 +441,8 @@ def svq_kv_assign(lens, n_new, page_size: int, block_table, free_pages, n_free, 
     import torch
     what = "svq_kv_assign"
     n, rows = lens.numel(), slots.numel()
-    _arrays(what, torch.int32, torch.cuda.current_device(), lens, n_new, block_table, free_pages, n_free, lens_out,
+    dev, st = _here(stream)
+    _arrays(what, torch.int32, dev, lens, n_new, block_table, free_pages, n_free, lens_out,
             n_free_out, cu_rows, positions, slots)
     _need(block_table.dim() == 2 and block_table.shape[0] == n and n_new.numel() == n and lens_out.numel() == n
           and cu_rows.numel() == n + 1 and positions.numel() == rows and n_free.numel() == 1
@@ -442,7 +450,7 @@ def svq_kv_assign(lens, n_new, page_size: int, block_table, free_pages, n_free, 
     _check(lib().svq_kv_assign(lens.data_ptr(), n_new.data_ptr(), n, page_size, block_table.data_ptr(),
                                block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
                                lens_out.data_ptr(), n_free_out.data_ptr(), cu_rows.data_ptr(), positions.data_ptr(),
-                               slots.data_ptr(), rows, _stream(stream)), what)
+                               slots.data_ptr(), rows, st), what)
 
 
 def svq_qk_norm_rope_cache(q, k, v, q_gamma, k_gamma, eps: float, rope: Rope, positions, slots, cache: KvCache, q_out,
@@ -451,24 +459,25 @@ def svq_qk_norm_rope_cache(q, k, v, q_gamma, k_gamma, eps: float, rope: Rope, po
     [M][n_q][D] and the cache's slots; gammas fp16 [D] or None; rows with a negative slot are left out."""
     import torch
     what = "svq_qk_norm_rope_cache"
-    M, D = q.shape[0], cache.head_dim
-    wq, wk = q_out.shape[1] * D, cache.n_heads * D
-    _need(q.shape == (M, wq) and k.shape == (M, wk) and v.shape == (M, wk) and q_out.shape[0] == M
-          and q_out.shape[2] == D and positions.numel() == M and slots.numel() == M, f"{what}: sizes do not agree")
-    _need(q.dtype == k.dtype == v.dtype and (M == 0 or q.stride(1) == k.stride(1) == v.stride(1) == 1), f"{what}: types or strides do not agree")
-    _need((q_gamma is None or q_gamma.numel() == D) and (k_gamma is None or k_gamma.numel() == D),
-          f"{what}: gamma must be [head_dim]")
-    dev = torch.cuda.current_device()
-    _need(q.get_device() == k.get_device() == v.get_device() == rope.device == cache.device == dev,
-          f"{what}: not on the current CUDA device")
+    D, wk = cache.head_dim, cache.n_heads * cache.head_dim
+    (M, wq), (Mk, wkk), (Mv, wkv), (Mo, heads, Do) = q.shape, k.shape, v.shape, q_out.shape
+    _need(Mk == Mv == Mo == M and wq == heads * D and wkk == wkv == wk and Do == D and positions.numel() == M
+          and slots.numel() == M and (q_gamma is None or q_gamma.numel() == D)
+          and (k_gamma is None or k_gamma.numel() == D), f"{what}: sizes do not agree")
+    (ldq, sq), (ldk, sk), (ldv, sv) = q.stride(), k.stride(), v.stride()
+    x = q.dtype
+    _need(k.dtype is x and v.dtype is x and (M == 0 or sq == sk == sv == 1), f"{what}: types or strides do not agree")
+    if M < 2:                                    # the distance between rows of one row says nothing
+        ldq, ldk, ldv = wq, wk, wk
+    dev, st = _here(stream)
+    _need(q.get_device() == dev and k.get_device() == dev and v.get_device() == dev and rope.device == dev
+          and cache.device == dev, f"{what}: not on the current CUDA device")
     _arrays(what, torch.int32, dev, positions, slots)
     _arrays(what, torch.float16, dev, q_gamma, k_gamma)
     _arrays(what, cache.dtype, dev, q_out)
-    ld = (q.stride(0), k.stride(0), v.stride(0)) if M > 1 else (wq, wk, wk)
-    _check(lib().svq_qk_norm_rope_cache(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(q.dtype), *ld, M,
-                                        q_out.shape[1], _opt(q_gamma), _opt(k_gamma), eps, rope._ref,
-                                        positions.data_ptr(), slots.data_ptr(), cache._ref, q_out.data_ptr(),
-                                        _stream(stream)), what)
+    _check(lib().svq_qk_norm_rope_cache(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(x), ldq, ldk, ldv, M,
+                                        heads, _opt(q_gamma), _opt(k_gamma), eps, rope._ref, positions.data_ptr(),
+                                        slots.data_ptr(), cache._ref, q_out.data_ptr(), st), what)
 
 
 def svq_paged_attention_workspace_size(cache: KvCache, n_q_heads: int) -> int:
@@ -491,7 +500,7 @@ def svq_paged_attention(q, cache: KvCache, lens, block_table, scale: float, out,
           and block_table.shape[0] == n and (cu_rows.numel() == n + 1 if cu_rows is not None else n <= rows)
           and (order is None or order.numel() == heads * D) and (lse is None or lse.shape == (rows, heads)),
           f"{what}: sizes do not agree")
-    dev = torch.cuda.current_device()
+    dev, st = _here(stream)
     _need(cache.device == dev, f"{what}: not on the current CUDA device")
     _arrays(what, cache.dtype, dev, q)
     _arrays(what, out.dtype, dev, out)
@@ -501,7 +510,7 @@ def svq_paged_attention(q, cache: KvCache, lens, block_table, scale: float, out,
     _check(lib().svq_paged_attention(q.data_ptr(), rows, heads, cache._ref, lens.data_ptr(), _opt(cu_rows), n,
                                      block_table.data_ptr(), block_table.shape[1], scale, _opt(order),
                                      out.data_ptr(), _dtype_code(out.dtype), _opt(lse), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), _stream(stream)), what)
+                                     ws.numel() * ws.element_size(), st), what)
 
 
 # ------------------------------------------------------------------ calibration (ESG, radius grid, encoder, ABS)

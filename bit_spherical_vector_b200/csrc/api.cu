@@ -486,6 +486,7 @@ int svq_kv_assign(const int32_t* lens, const int32_t* n_new, int n_seqs, int pag
   p.lens = lens; p.n_new = n_new; p.table = block_table; p.free_pages = free_pages; p.n_free = n_free;
   p.lens_out = lens_out; p.n_free_out = n_free_out; p.cu_rows = cu_rows; p.positions = positions; p.slots = slots;
   p.status = status;
+  p.by_page = svq::FastDiv(page_size);
   p.n_seqs = n_seqs; p.width = max_pages; p.page_size = page_size; p.n_pages = n_pages; p.max_rows = max_rows;
   return cuda_status(svq::launch_kv_assign(p, (cudaStream_t)stream));
 }

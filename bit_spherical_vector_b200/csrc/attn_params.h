@@ -27,6 +27,7 @@ struct KvAssignParams {
   int32_t* positions;                    // [max_rows]
   int32_t* slots;                        // [max_rows]
   int32_t* status;
+  FastDiv by_page;
   int n_seqs, width, page_size, n_pages, max_rows;
 };
 cudaError_t launch_kv_assign(const KvAssignParams& p, cudaStream_t st);
