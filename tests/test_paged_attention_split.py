@@ -134,7 +134,7 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
   split_units += (long long)far.size();
   // The joins: CTAs arrive in random order, the last of a group adds its parts and goes on for them.
   static std::mt19937 shuffle(11);
-  for (int fan : {8, 16, 128}) {
+  for (int fan : {8, 16, 32}) {
     std::map<std::pair<int, int>, std::pair<long long, int>> at;       // (level, counter) -> unit, arrivals
     for (auto& f : far) {
       const int c0 = *f.second.begin(), n = (int)f.second.size();
