@@ -95,21 +95,72 @@ struct AttnCursor {
   SVQ_HD int unit(int heads) const { return b * heads + h; }   // at most 2^22
 };
 
-// Tiles [s0, s1) of a CTA: one unit (short requests, as many CTAs as units), or
-// its range of the even split.  False: none.
-SVQ_HD bool attn_share(const AttnSeqs& s, int n, int heads, const FastDiv& by_heads, bool by_unit, const AttnLine& line,
-                       int cta, long long* s0, long long* s1) {
-  if (by_unit) {
-    if (cta >= n * heads) return false;
-    const int b = by_heads.div(cta), nt = s.tiles(b);
-    *s0 = (long long)s.pre[b] * heads + (long long)(cta - b * heads) * nt;
-    *s1 = *s0 + nt;
-    return nt > 0;
-  }
-  if (cta >= line.n) return false;
-  *s0 = line.start(cta);
-  *s1 = line.start(cta + 1);
-  return *s1 > *s0;
+// A range boundary moved to the nearer end of the unit that it would cut, if the
+// unit has at most `most` tiles (a cut costs a join).  Places at the line's end stay.
+SVQ_HD long long attn_snap(const AttnSeqs& s, int n, int heads, const FastDiv& by_heads, long long total, int most,
+                           long long g) {
+  if (g <= 0 || g >= total) return g;
+  AttnCursor c;
+  c.set(s, n, heads, by_heads, g);
+  if (c.nt > most) return g;
+  return 2 * c.t <= c.nt ? g - c.t : g - c.t + c.nt;
 }
+
+// Longest units that boundaries do not cut: what a boundary moves is read by one
+// SM or warp more and another less, so only units of a few tiles, and for warps of
+// at most twice their share, are worth it.
+constexpr int kSnap = 8;
+SVQ_HD int attn_warp_snap(long long tiles, int warps) {
+  const long long share = 2 * tiles / warps;
+  return share < kSnap ? (int)share : kSnap;
+}
+
+// The cut of the line: `by_unit` gives each unit to a CTA (short requests, as many
+// CTAs as units), else CTAs and their warps get even ranges but for the short units
+// at their ends, if there are any (`shorts`).
+struct AttnCut {
+  AttnSeqs s;
+  AttnLine line;
+  FastDiv by_heads;
+  long long total;
+  int n, heads;
+  bool by_unit, shorts;
+  SVQ_HD AttnCut(const AttnSeqs& seqs, int n_seqs, int n_heads, const FastDiv& div, bool unit_each, bool any_short,
+                 int grid, int warps)
+      : s(seqs),
+        line((long long)seqs.pre[n_seqs] * n_heads, attn_ctas((long long)seqs.pre[n_seqs] * n_heads, grid, warps)),
+        by_heads(div),
+        total((long long)seqs.pre[n_seqs] * n_heads),
+        n(n_seqs),
+        heads(n_heads),
+        by_unit(unit_each),
+        shorts(any_short) {}
+  SVQ_HD bool moves() const { return shorts && !by_unit; }         // edges are not simply the even ranges
+  SVQ_HD int ctas() const { return by_unit ? n * heads : line.n; }
+  // First place of CTA c's range, 0 <= c <= ctas() (a range may be empty).
+  SVQ_HD long long edge(int c) const {
+    if (!by_unit) {
+      const long long g = line.start(c);
+      return moves() ? attn_snap(s, n, heads, by_heads, total, kSnap, g) : g;
+    }
+    const int b = by_heads.div(c);
+    return b == n ? total : (long long)s.pre[b] * heads + (long long)(c - b * heads) * s.tiles(b);
+  }
+  // First place of warp w's range in the CTA's [s0, s1), 0 <= w <= warps.
+  SVQ_HD long long warp_edge(long long s0, long long s1, int w, int warps) const {
+    if (w == 0) return s0;
+    if (w == warps) return s1;
+    const AttnLine part(s1 - s0, warps);
+    long long g = s0 + part.start(w);
+    if (!moves()) return g;
+    g = attn_snap(s, n, heads, by_heads, total, attn_warp_snap(s1 - s0, warps), g);
+    return g < s0 ? s0 : g > s1 ? s1 : g;
+  }
+  // CTAs that share the unit of tiles [u0, u1) if any boundary cuts it.  Boundaries
+  // inside such a unit have not been moved and others not into it, so they are those
+  // that the even ranges give.
+  SVQ_HD int first_cta(long long u0) const { return line.range_of(u0); }
+  SVQ_HD int last_cta(long long u1) const { return line.range_of(u1 - 1); }
+};
 
 }  // namespace svq

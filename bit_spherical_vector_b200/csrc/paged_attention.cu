@@ -159,19 +159,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   __shared__ UnitOut part_to[P];
   __shared__ int part_unit[P];                                     // unit of a part, -1: none
   __shared__ int2 note[W][S::kStages];                             // tile in a stage: keys that count and flags; unit
-  __shared__ int wsum[W];
+  __shared__ int2 wsum[W];
   __shared__ bool joined[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.n_seqs, heads = p.kv.n_heads * p.row_tiles;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- prefix sums of the requests' tiles
-  bool any_long, any_empty;                                // requests of more than kUnitTiles tiles, rows without a key
+  int kinds;                                               // of requests that the call has
+  constexpr int kLong = 1, kEmpty = 2, kShort = 4;         // more than kUnitTiles tiles, a row but no key, 1 to kSnap tiles
   {
     const int per = (n + T - 1) / T, b0 = min(n, tid * per), b1 = min(n, b0 + per);
     const int most = p.width * p.kv.page_size;
     int sum = 0;
-    bool is_long = false, is_empty = false;
+    kinds = 0;
     for (int b = b0; b < b1; ++b) {
       int len = p.lens[b], row = b;
       bool skip = false;
@@ -193,8 +194,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       pre[b] = nt;
       meta[b] = skip ? kNoRow : ((uint32_t)row << 4) | (uint32_t)(nt * kTile - len);
       sum += nt;
-      is_long |= nt > S::kUnitTiles;
-      is_empty |= !skip && nt == 0;
+      kinds |= nt > S::kUnitTiles ? kLong : nt > kSnap ? 0 : nt > 0 ? kShort : skip ? 0 : kEmpty;
     }
     int inc = sum;
 #pragma unroll
@@ -202,14 +202,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       const int v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
       if (lane >= o) inc += v;
     }
-    if (lane == 31) wsum[warp] = inc;
-    any_long = __syncthreads_or(is_long);
+    kinds = __reduce_or_sync(0xFFFFFFFFu, kinds);
+    if (lane == 31) wsum[warp] = make_int2(inc, kinds);
+    __syncthreads();
     int before = inc - sum, all = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const int v = wsum[w];
-      before += w < warp ? v : 0;
-      all += v;
+      const int2 v = wsum[w];
+      before += w < warp ? v.x : 0;
+      all += v.x;
+      kinds |= v.y;
     }
     for (int b = b0; b < b1; ++b) {
       const int nt = pre[b];
@@ -217,25 +219,37 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       before += nt;
     }
     if (tid == 0) pre[n] = all;
-    any_empty = __syncthreads_or(is_empty);
+    __syncthreads();
   }
   const AttnSeqs seqs{pre, meta};
   // rows without a key: zeros, and the logarithm of an empty sum
-  for (int b = blockIdx.x; any_empty && b < n; b += gridDim.x) {
+  for (int b = blockIdx.x; (kinds & kEmpty) && b < n; b += gridDim.x) {
     if (seqs.tiles(b) != 0 || meta[b] == kNoRow) continue;
     const int64_t row = seqs.row(b);
     for (int i = tid; i < p.n_q * (D / 2); i += T) reinterpret_cast<uint32_t*>(p.out + row * p.n_q * D)[i] = 0u;
     if (p.lse)
       for (int i = tid; i < p.n_q; i += T) p.lse[row * p.n_q + i] = kNegInf;
   }
-  const long long total = (long long)pre[n] * heads;
   const int cta = blockIdx.x;
-  const bool by_unit = !any_long && n * heads <= (int)gridDim.x;
-  const AttnLine line(total, attn_ctas(total, gridDim.x, W));
-  long long s0, s1;
-  if (!attn_share(seqs, n, heads, p.by_heads, by_unit, line, cta, &s0, &s1)) return;
-  const AttnLine part(s1 - s0, W);
-  const long long w0 = s0 + part.start(warp), w1 = s0 + part.start(warp + 1);
+  const AttnCut cut(seqs, n, heads, p.by_heads, !(kinds & kLong) && n * heads <= (int)gridDim.x, kinds & kShort,
+                    gridDim.x, W);
+  if (cta >= cut.ctas()) return;
+  long long s0, s1, w0, w1;                                // tiles of this CTA, of this warp
+  if (cut.moves()) {                                       // two edges, each with a search: side by side in two lanes
+    long long edge = cut.edge(cta + (lane & 1));
+    s0 = __shfl_sync(0xFFFFFFFFu, edge, 0);
+    s1 = __shfl_sync(0xFFFFFFFFu, edge, 1);
+    edge = cut.warp_edge(s0, s1, warp + (lane & 1), W);
+    w0 = __shfl_sync(0xFFFFFFFFu, edge, 0);
+    w1 = __shfl_sync(0xFFFFFFFFu, edge, 1);
+  } else {
+    s0 = cut.edge(cta);
+    s1 = cut.edge(cta + 1);
+    const AttnLine part(s1 - s0, W);
+    w0 = s0 + part.start(warp);
+    w1 = s0 + part.start(warp + 1);
+  }
+  if (s1 <= s0) return;
 
   const uint32_t ring = sm100::smem_u32(smem) + warp * S::kStages * S::kStage;
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
@@ -381,8 +395,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
         to.heads = (kv_head * p.group + rt * R) << 8 | count;
         to.c0 = to.c1 = cta;
         if (u0 < s0 || u1 > s1) {
-          to.c0 = line.range_of(u0);
-          to.c1 = line.range_of(u1 - 1);
+          to.c0 = cut.first_cta(u0);
+          to.c1 = cut.last_cta(u1);
         }
         const uint16_t* qr = p.q + ((int64_t)to.row * p.n_q + (to.heads >> 8)) * D;
 #pragma unroll

@@ -40,11 +40,13 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
   const AttnSeqs s{pre.data(), meta.data()};
   for (int b = 0; b < n; ++b) CHECK(s.len(b) == lens[b] && s.row(b) == b, "meta %d", b);
   const long long total = (long long)pre[n] * heads;
-  const AttnLine line(total, attn_ctas(total, grid, W));
   const FastDiv by_heads(heads);
   int longest = 0;
   for (int b = 0; b < n; ++b) longest = std::max(longest, s.tiles(b));
   const bool by_unit = longest <= 4 * W && (long long)n * heads <= grid;
+  bool shorts = false;
+  for (int b = 0; b < n; ++b) shorts |= s.tiles(b) > 0 && s.tiles(b) <= kSnap;
+  const AttnCut cut(s, n, heads, by_heads, by_unit, shorts, grid, W);
   ++cases;
   units += by_unit;
   std::map<long long, int> written;                       // unit -> times written
@@ -52,14 +54,16 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
   std::map<long long, std::set<int>> far;                 // unit -> CTAs that left a part
   long long expect_b = 0, expect_h = 0, expect_t = -1;    // the line in order
   int eb = -1;
-  for (int c = 0; c < grid; ++c) {
-    long long s0, s1;
-    if (!attn_share(s, n, heads, by_heads, by_unit, line, c, &s0, &s1)) continue;
-    const AttnLine share(s1 - s0, W);
-    CHECK(s1 > s0, "empty CTA");
+  CHECK(cut.ctas() <= grid && cut.edge(0) == 0 && cut.edge(cut.ctas()) == total, "ends of the line");
+  for (int c = 0; c < cut.ctas(); ++c) {
+    const long long s0 = cut.edge(c), s1 = cut.edge(c + 1);
+    CHECK(s1 >= s0, "CTA ranges overlap");
+    if (s1 <= s0) continue;
+    CHECK(cut.warp_edge(s0, s1, 0, W) == s0 && cut.warp_edge(s0, s1, W, W) == s1, "ends of a CTA");
     std::vector<long long> part(2 * W, -1);
     for (int w = 0; w < W; ++w) {
-      const long long w0 = s0 + share.start(w), w1 = s0 + share.start(w + 1);
+      const long long w0 = cut.warp_edge(s0, s1, w, W), w1 = cut.warp_edge(s0, s1, w + 1, W);
+      CHECK(s0 <= w0 && w0 <= w1 && w1 <= s1, "warp ranges overlap");
       if (w0 >= w1) continue;
       AttnCursor cur;
       bool fresh = true, from_start = true;
@@ -119,7 +123,7 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
         const int slot = u0 >= s0;
         CHECK(!used[slot], "workspace slot twice");
         used[slot] = true;
-        const int c0 = line.range_of(u0), c1 = line.range_of(u1 - 1);
+        const int c0 = cut.first_cta(u0), c1 = cut.last_cta(u1);
         CHECK(!by_unit && c0 <= c && c <= c1 && c1 > c0, "CTAs of a unit");
         CHECK((slot == 1) == (c == c0), "slot of the first CTA");
         CHECK(far[unit].insert(c).second, "two parts of a unit in one CTA");
@@ -182,7 +186,7 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
 int main() {
   std::mt19937 r(7);
   auto u = [&](int a, int b) { return a + (int)(r() % (unsigned)(b - a + 1)); };
-  for (int W : {4, 8})
+  for (int W : {4, 8, 12})
     for (int len : {0, 1, 15, 16, 17, 127, 128, 512, 4096, 40000})
       for (int heads : {1, 8})
         walk({len}, heads, 148, W);
@@ -190,7 +194,7 @@ int main() {
     const int n = u(1, i % 10 ? 40 : 600), heads = u(1, i % 7 ? 8 : 64), most = 1 << u(2, 12);
     std::vector<int> lens(n);
     for (auto& l : lens) l = u(0, 4) ? u(0, most) : 0;
-    walk(lens, heads, i % 3 ? 148 : u(1, 160), u(0, 1) ? 8 : 4);
+    walk(lens, heads, i % 3 ? 148 : u(1, 160), i % 4 == 0 ? 4 : i % 4 == 1 ? 12 : 8);
   }
   // ranges far beyond 32 bits
   for (int i = 0; i < 2000; ++i) {
