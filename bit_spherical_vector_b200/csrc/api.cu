@@ -550,6 +550,7 @@ int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_
   if (n_seqs > svq::kMaxSeqs || n_rows > (1 << 26) || (int64_t)max_pages * cache->page_size > INT32_MAX ||
       n_seqs * ((int64_t)max_pages * cache->page_size / 16 + 1) > INT32_MAX || n_q_heads > 1024)
     return SVQ_ERR_UNSUPPORTED_SHAPE;
+  if (order && (int64_t)n_q_heads * cache->head_dim > svq::kMaxOrdered) return SVQ_ERR_UNSUPPORTED_SHAPE;
   svq::PagedAttnPlan plan;
   const int sms = num_sms();
   if (n_q_heads < 1 || n_q_heads % cache->n_heads != 0) return SVQ_ERR_UNSUPPORTED_SHAPE;
@@ -557,7 +558,7 @@ int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !lens || !aligned(lens, 4) || !block_table ||
       !aligned(block_table, 4))
     return SVQ_ERR_INVALID_ARG;
-  if ((cu_rows && !aligned(cu_rows, 4)) || (order && !aligned(order, 4)) || (lse && !aligned(lse, 4)))
+  if ((cu_rows && !aligned(cu_rows, 4)) || (order && !aligned(order, 16)) || (lse && !aligned(lse, 4)))
     return SVQ_ERR_INVALID_ARG;
   if (sms <= 0) return SVQ_ERR_CUDA;
   if (!svq::plan_paged_attn(n_q_heads, cache->n_heads, cache->head_dim, n_seqs, sms, &plan))

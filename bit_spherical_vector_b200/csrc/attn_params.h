@@ -13,6 +13,7 @@
 
 namespace svq {
 
+constexpr int kMaxOrdered = 65536;       // entries of an output row that is written in another order
 constexpr int kMaxSeqs = 4096;           // requests of one call (their prefix sums stay in shared memory)
 
 struct KvAssignParams {
@@ -108,9 +109,9 @@ cudaError_t allow_smem(Kern kern, size_t bytes, std::atomic<int> (&have)[64]) {
 
 // Launch with programmatic stream serialization (the kernel waits with
 // griddepcontrol.wait) and, for cluster > 1, as clusters of that many CTAs.
-template <typename Kern, typename P>
+template <typename Kern, typename... P>
 cudaError_t launch_dependent(Kern kern, dim3 grid, unsigned threads, size_t smem, unsigned cluster,
-                             cudaStream_t st, const P& p) {
+                             cudaStream_t st, const P&... p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -125,7 +126,7 @@ cudaError_t launch_dependent(Kern kern, dim3 grid, unsigned threads, size_t smem
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p...);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

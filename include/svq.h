@@ -472,14 +472,16 @@ SVQ_API int svq_qk_norm_rope_cache(const void* q, const void* k, const void* v, 
  * the cache and the table behind a request's length are not looked at.
  * q: [n_rows][n_q_heads][head_dim] of the cache's type.  out: [n_rows][n_q_heads *
  * head_dim] of out_dtype SVQ_F16 or SVQ_BF16, entry s = h * head_dim + d at column
- * order[s] (device int32 [n_q_heads * head_dim]; NULL: s).  With order the inverse of
- * o's perm (order[perm[j]] = j) the row is o's input in its stored column order,
- * for a descriptor with perm NULL.  lse: fp32 [n_rows][n_q_heads] natural
+ * order[s] (device int32 [n_q_heads * head_dim], 16-byte aligned; NULL: s).  With
+ * order the inverse of o's perm (order[perm[j]] = j) the row is o's input in its
+ * stored column order, for a descriptor with perm NULL; n_q_heads * head_dim is then
+ * at most 65536, and a second kernel reorders the rows.  A column that no entry
+ * goes to is 0.  lse: fp32 [n_rows][n_q_heads] natural
  * logarithm of the sum of e^s, or NULL.
  * Lengths, rows, page numbers and order are checked on the device: a length
  * outside 0..max_pages * page_size is clamped, a row outside 0..n_rows-1 is left
- * out, a key on a page outside the pool does not count, an entry of order outside
- * the row is not written; each sets the device status word to SVQ_ERR_INVALID_ARG.
+ * out, a key on a page outside the pool does not count, an entry that order sends
+ * outside the row is dropped; each sets the device status word to SVQ_ERR_INVALID_ARG.
  * n_seqs <= 4096 and n_seqs * (max_pages * page_size / 16 + 1) < 2^31.
  * Workspace (svq_paged_attention_workspace_size; the lengths and n_seqs do not
  * matter): completion counters in its first 64 KiB, zero before the first call

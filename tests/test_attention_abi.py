@@ -90,7 +90,7 @@ def test_no_rows_is_a_no_op():
     (dict(rows=-1), INV), (dict(width=0), INV), (dict(n=4097), SHAPE), (dict(width=1 << 27), SHAPE),
     (dict(n=4096, width=1 << 20), SHAPE), (dict(n_q=0), SHAPE), (dict(n_q=7), SHAPE), (dict(n_q=1026), SHAPE),
     (dict(q=None), INV), (dict(q=0x1008), INV), (dict(out=0x1002), INV), (dict(lens=None), INV), (dict(lens=0x1002), INV),
-    (dict(table=None), INV), (dict(cu=0x1001), INV), (dict(order=0x1002), INV), (dict(lse=0x1002), INV)])
+    (dict(table=None), INV), (dict(cu=0x1001), INV), (dict(order=0x1008), INV), (dict(order=A, n_q=514), SHAPE), (dict(lse=0x1002), INV)])
 def test_paged_attention_refusals(kw, status):
     assert call_attn(**kw) == status
 

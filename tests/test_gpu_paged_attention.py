@@ -227,7 +227,7 @@ def test_bad_pages_lengths_rows_and_columns():
         d["order"][7] = 4 * 64
         svq.svq_paged_attention(**d)
         assert svq.svq_get_device_status() == svq.SVQ_ERR_INVALID_ARG
-        assert bool((d["out"][:, gone] == 3.0).all()) and int((d["out"] == 3.0).sum()) == 2
+        assert bool((d["out"][:, gone] == 0.0).all()) and not bool((d["out"] == 3.0).any())
 
 
 def test_pool_beyond_32_bit_offsets():
