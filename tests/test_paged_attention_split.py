@@ -186,7 +186,7 @@ static void walk(const std::vector<int>& lens, int heads, int grid, int W) {
 int main() {
   std::mt19937 r(7);
   auto u = [&](int a, int b) { return a + (int)(r() % (unsigned)(b - a + 1)); };
-  for (int W : {4, 8, 12})
+  for (int W : {4, 8, 10})
     for (int len : {0, 1, 15, 16, 17, 127, 128, 512, 4096, 40000})
       for (int heads : {1, 8})
         walk({len}, heads, 148, W);
@@ -194,7 +194,7 @@ int main() {
     const int n = u(1, i % 10 ? 40 : 600), heads = u(1, i % 7 ? 8 : 64), most = 1 << u(2, 12);
     std::vector<int> lens(n);
     for (auto& l : lens) l = u(0, 4) ? u(0, most) : 0;
-    walk(lens, heads, i % 3 ? 148 : u(1, 160), i % 4 == 0 ? 4 : i % 4 == 1 ? 12 : 8);
+    walk(lens, heads, i % 3 ? 148 : u(1, 160), i % 4 == 0 ? 4 : i % 4 == 1 ? 10 : 8);
   }
   // ranges far beyond 32 bits
   for (int i = 0; i < 2000; ++i) {
