@@ -769,10 +769,12 @@ def run_calib(args, quiet=False):
 
 def run_chain(args):
     """Qwen3-4B decoder-layer chain at batch 1 and 4: the layer's linears in dependency order with their
-    producers (norm -> q|k|v, o, norm -> gate|up, SiLU-gated product -> down; attention itself is not part of
-    the chain, o reads a synthetic attention output).  Two variants: the producers write x in natural order
-    and every SVQ call gathers x[perm] ("gather"), or the producers write each consumer's stored order and the
-    SVQ calls take perm NULL ("stored").  14 rotated layer copies (inputs larger than L2)."""
+    producers (norm -> q|k|v, o, norm -> gate|up, SiLU-gated product -> down; o reads a synthetic attention
+    output).  Two variants: the producers write x in natural order and every SVQ call gathers x[perm] ("gather"),
+    or the producers write each consumer's stored order and the SVQ calls take perm NULL ("stored").  A third
+    ("with_attention") is "gather" with the attention step in place: head norms and rotary positions into a
+    paged cache and decode attention over 1024 keys a request, o reading its output.  14 rotated layer copies
+    (inputs larger than L2), a cache for each."""
     import torch
     import bit_spherical_vector_b200 as svq
     stream = torch.cuda.Stream()
@@ -831,20 +833,52 @@ def run_chain(args):
                 svq.svq_swiglu_permute(ys[4], ys[5], Ws[6].perm, xd)
                 svq.svq_linear_gemv(Wn[6], xd, ys[6], ws)
 
+        keys, page = 1024, 16
+        caches, table = [], torch.randperm(M * (keys // page), device="cuda").to(torch.int32).view(M, keys // page)
+        for _ in range(N_LAYERS):
+            kv = [torch.randn((M * (keys // page), page, 8, 128), device="cuda").half() for _ in range(2)]
+            caches.append(svq.KvCache(*kv))
+        rope = svq.Rope.make(128, 1e6)
+        gq, gk = f16(rng.uniform(0.5, 1.5, 128)), f16(rng.uniform(0.5, 1.5, 128))
+        lens = torch.full((M,), keys, dtype=torch.int32, device="cuda")
+        pos = torch.full((M,), keys - 1, dtype=torch.int32, device="cuda")
+        slots = table[:, -1].contiguous() * page + page - 1
+        q_rot = torch.empty((M, 32, 128), dtype=torch.float16, device="cuda")
+        att_out = e16(4096)
+        wa = torch.empty(svq.svq_paged_attention_workspace_size(caches[0], 32), dtype=torch.uint8, device="cuda")
+        with torch.cuda.stream(stream):
+            svq.svq_workspace_init(wa)
+        torch.cuda.synchronize()
+
+        def with_attention():
+            for (Ws, _), cache in zip(layers, caches):
+                svq.svq_rmsnorm_permute(h1, g1, eps, [None], [xn])
+                svq.svq_linear_gemv_batched(Ws[0:3], [xn] * 3, ys[0:3], ws)
+                svq.svq_qk_norm_rope_cache(*ys[0:3], gq, gk, eps, rope, pos, slots, cache, q_rot)
+                svq.svq_paged_attention(q_rot, cache, lens, table, 128 ** -0.5, att_out, wa)
+                svq.svq_linear_gemv(Ws[3], att_out, ys[3], ws)
+                svq.svq_rmsnorm_permute(h2, g2, eps, [None], [xn2])
+                svq.svq_linear_gemv_batched(Ws[4:6], [xn2] * 2, ys[4:6], ws)
+                svq.svq_swiglu_permute(ys[4], ys[5], None, xd)
+                svq.svq_linear_gemv(Ws[6], xd, ys[6], ws)
+
         def one_launch():
             for Ws, _ in layers:
                 svq.svq_linear_gemv_batched(Ws, [xn] * 3 + [att, xn2, xn2, xd], ys, ws)
 
         res = {}
-        for name, fn in (("one_launch", one_launch), ("gather", gather), ("stored", stored), ("stored_o", stored_o)):
+        for name, fn in (("one_launch", one_launch), ("gather", gather), ("stored", stored), ("stored_o", stored_o),
+                         ("with_attention", with_attention)):
             res[name] = _time_graph(fn, 50, stream) / N_LAYERS
         print(json.dumps({"workload": "qwen3-4b decoder-layer chain", "M": M,
                           "us_per_layer": {k: round(v, 2) for k, v in res.items()},
                           "GBps_packed": {k: round(packed_b / v / 1e3, 1) for k, v in res.items()},
-                          "launches_per_layer": {"one_launch": 1, "gather": 7, "stored": 7, "stored_o": 7},
+                          "launches_per_layer": {"one_launch": 1, "gather": 7, "stored": 7, "stored_o": 7,
+                                                 "with_attention": 9},
                           "note": "one_launch = the seven linears in one grouped launch without their data "
                                   "dependencies (the headline); gather/stored = dependency order with producers; "
-                                  "stored_o = stored with the attention output also in o's stored order"}),
+                                  "stored_o = stored with the attention output also in o's stored order; "
+                                  "with_attention = gather with the attention step over 1024 keys a request"}),
               flush=True)
 
 
