@@ -547,7 +547,7 @@ int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_
   if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return SVQ_ERR_INVALID_ARG;      // rejects NaN and infinities
   if (n_seqs < 0 || n_rows < 0 || max_pages < 1) return SVQ_ERR_INVALID_ARG;
   // the tiles of all requests are counted in 32 bits
-  if (n_seqs > svq::kMaxSeqs || n_rows > (1 << 26) || (int64_t)max_pages * cache->page_size > INT32_MAX ||
+  if (n_seqs > svq::kMaxSeqs || n_rows > (1 << 26) || (int64_t)max_pages * cache->page_size > INT32_MAX - 16 ||
       n_seqs * ((int64_t)max_pages * cache->page_size / 16 + 1) > INT32_MAX || n_q_heads > 1024)
     return SVQ_ERR_UNSUPPORTED_SHAPE;
   if (order && (int64_t)n_q_heads * cache->head_dim > svq::kMaxOrdered) return SVQ_ERR_UNSUPPORTED_SHAPE;

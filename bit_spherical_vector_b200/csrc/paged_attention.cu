@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   int* pre = reinterpret_cast<int*>(smem + S::kRing);
   uint32_t* meta = reinterpret_cast<uint32_t*>(pre + p.n_seqs + 1);
   constexpr int P = 2 * W;                                         // parts of a CTA at most: two per warp
-  static_assert(P * R <= T, "one thread for each part and head");
+  static_assert(P <= 32, "one lane for each part");
   __shared__ float2 part_ml[P][R];                                 // (maximum, sum) of a part
   __shared__ UnitOut part_to[P];
   __shared__ int part_unit[P];                                     // unit of a part, -1: none
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       int keys = min(kTile, seqs.len(c.b) - at_key);
       if (whole) {
         const int j = p.by_page.div(at_key);
-        const int page = __ldg(p.table + (int64_t)c.b * p.width + j);
+        const int page = p.table[(int64_t)c.b * p.width + j];
         if ((unsigned)page < (unsigned)p.kv.n_pages) {
           at_base += (int64_t)page * p.kv.page_stride + (int64_t)(at_key - j * p.kv.page_size) * p.kv.token_stride;
         } else {                                           // keys on a page that does not exist do not count
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
         int64_t mine = 0;
         bool ok = false;
         if ((lane & 15) < keys) {
-          const int page = __ldg(p.table + (int64_t)req * p.width + j);
+          const int page = p.table[(int64_t)req * p.width + j];
           ok = (unsigned)page < (unsigned)p.kv.n_pages;
           if (ok) mine = (int64_t)page * p.kv.page_stride + (int64_t)(key - j * p.kv.page_size) * p.kv.token_stride;
           else *p.status = SVQ_ERR_INVALID_ARG;
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
       const float f = lane % kLanes < members ? part_weight(ml.x, M) : 0.f;
-      float L = f == 0.f ? 0.f : f * ml.y;
+      float L = lane % kLanes < members ? f * ml.y : 0.f;
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xFFFFFFFFu, L, o);
       float4 acc[V];

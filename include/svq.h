@@ -349,8 +349,8 @@ SVQ_API int svq_swiglu_permute(const float* gate, const float* up, int M, int I,
  * paged key/value cache.  The pages evaluate SVQ inside Qwen3 models (abstract)
  * without describing their attention; the formulas are stated with each call.
  * All calls are launched as programmatic dependents like the GEMV, read their
- * inputs only after the previous kernel on `stream` has completed (gammas and
- * inv_freq may be read earlier: they are weights), and write results that do
+ * inputs only after the previous kernel on `stream` has completed (gammas,
+ * inv_freq and order may be read earlier: they are weights), and write results that do
  * not depend on timing.
  *
  * svq_kv_cache -- a pool of pages for keys and one for values: entry d of key
@@ -398,6 +398,7 @@ typedef struct svq_kv_cache {
  * SVQ_ERR_INVALID_ARG.  A page number outside 0..n_pages-1 in the table or the
  * list gives slot -1 and sets the status word.  n_pages * page_size, max_pages *
  * page_size and n_seqs * max_pages < 2^31, max_rows <= 2^30.
+ * But for the two named pairs no array may overlap another.
  */
 SVQ_API int svq_kv_assign(const int32_t* lens, const int32_t* n_new, int n_seqs, int page_size,
                           int32_t* block_table, int max_pages, int32_t* free_pages, int n_pages,
@@ -482,7 +483,9 @@ SVQ_API int svq_qk_norm_rope_cache(const void* q, const void* k, const void* v, 
  * outside 0..max_pages * page_size is clamped, a row outside 0..n_rows-1 is left
  * out, a key on a page outside the pool does not count, an entry that order sends
  * outside the row is dropped; each sets the device status word to SVQ_ERR_INVALID_ARG.
- * n_seqs <= 4096 and n_seqs * (max_pages * page_size / 16 + 1) < 2^31.
+ * n_seqs <= 4096, max_pages * page_size < 2^31 - 16 and n_seqs * (max_pages *
+ * page_size / 16 + 1) < 2^31.  out, lse and the workspace must not overlap the
+ * inputs or each other.
  * Workspace (svq_paged_attention_workspace_size; the lengths and n_seqs do not
  * matter): completion counters in its first 64 KiB, zero before the first call
  * (svq_workspace_init), left zero by every completed call, then parts of split

@@ -200,6 +200,11 @@ def test_nan_in_a_key_that_counts_is_seen():
     out = a["out"].view(2, 4, 64)
     assert bool(torch.isnan(out[0, :2]).all()) and bool(torch.isfinite(out[0, 2:]).all())
     assert bool(torch.isfinite(out[1]).all())
+    for lens in ([40], [4000]):                                # nothing but NaN, whole and joined
+        a = case(8, lens, 4, 2, 64)
+        a["cache"].k.fill_(float("nan"))
+        svq.svq_paged_attention(**a)
+        assert bool(torch.isnan(a["out"]).all()) and bool(torch.isnan(a["lse"]).all())
 
 
 def test_bad_pages_lengths_rows_and_columns():
