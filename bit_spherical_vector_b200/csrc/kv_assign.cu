@@ -166,36 +166,71 @@ __global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_consta
   }
   const Stack stack{p, gone, n_free};
   const int itop = (int)top;
-  for (int r = g; r < p.max_rows; r += gn) {
-    int pos = -1, slot = -1;
-    if (r < (int)rows_all) {
-      const int b = find_segment(cu, n, r);
-      const int l = len[b];
-      pos = l + (r - cu[b]);
-      const int held = pages_of(l), j = p.by_page.div(pos);
-      const int page = j < held ? p.table[(size_t)b * p.width + j] : stack.at(itop - 1 - (need[b] + j - held));
-      if ((unsigned)page < (unsigned)p.n_pages) slot = page * ps + (pos - j * ps);
-      else *p.status = SVQ_ERR_INVALID_ARG;
+  // Four entries at a time: their loads are on their way together before the first store.
+  constexpr int kBatch = 4;
+  for (int r0 = g; r0 < p.max_rows; r0 += kBatch * gn) {
+    int pos[kBatch], page[kBatch], off[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * gn;
+      pos[k] = -1;
+      page[k] = off[k] = 0;
+      if (r >= (int)rows_all) continue;
+      const int b = find_segment(cu, n, r), l = len[b];
+      pos[k] = l + (r - cu[b]);
+      const int held = pages_of(l), j = p.by_page.div(pos[k]);
+      off[k] = pos[k] - j * ps;
+      page[k] = j < held ? p.table[(size_t)b * p.width + j] : stack.at(itop - 1 - (need[b] + j - held));
     }
-    p.positions[r] = pos;
-    p.slots[r] = slot;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + k * gn;
+      if (r >= p.max_rows) break;
+      const bool ok = (unsigned)page[k] < (unsigned)p.n_pages;
+      if (!ok) *p.status = SVQ_ERR_INVALID_ARG;
+      p.positions[r] = pos[k];
+      p.slots[r] = pos[k] >= 0 && ok ? page[k] * ps + off[k] : -1;
+    }
   }
-  for (int k = g; k < need_all; k += gn) {
-    const int b = find_segment(need, n, k);
-    const int held = pages_of(len[b]);
-    p.table[(size_t)b * p.width + held + (k - need[b])] = stack.at(itop - 1 - k);
+  for (int k0 = g; k0 < need_all; k0 += kBatch * gn) {
+    int at[kBatch], page[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = k0 + k * gn;
+      at[k] = page[k] = 0;
+      if (i >= need_all) continue;
+      const int b = find_segment(need, n, i);
+      at[k] = b * p.width + pages_of(len[b]) + (i - need[b]);
+      page[k] = stack.at(itop - 1 - i);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (k0 + k * gn < need_all) p.table[at[k]] = page[k];
   }
   // released pages that the step does not take go onto the list
-  for (int i = n_free + g; i < itop - need_all; i += gn) p.free_pages[i] = stack.released(i - n_free);
+  for (int i0 = n_free + g; i0 < itop - need_all; i0 += kBatch * gn) {
+    int page[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * gn;
+      page[k] = i < itop - need_all ? stack.released(i - n_free) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k * gn < itop - need_all) p.free_pages[i0 + k * gn] = page[k];
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_assign(const KvAssignParams& p, cudaStream_t st) {
   const size_t smem = (size_t)(4 * p.n_seqs + 3) * sizeof(int);
-  // Two rows a thread are as quick on one CTA as on a cluster (16 decode rows 2.8 us);
-  // beyond, a cluster is quicker (543 requests and 3339 rows: 4.8 us against 6.9 us).
-  const unsigned ctas = p.max_rows > 2 * kThreads ? 8 : 1;
+  // One CTA where there is little to spread, which a cluster makes 0.2 us slower (16
+  // decode rows: 2.9 us against 3.1 us); a cluster where rows are many (543 requests
+  // and 3339 rows: 4.8 us against 6.9 us) or the table is large, since a done request
+  // may release a long row of it (63 requests of up to 3909 pages: 7.5 us against 30 us).
+  const bool small = p.max_rows <= 2 * kThreads && (long long)p.n_seqs * p.width <= 8192;
+  const unsigned ctas = small ? 1 : 8;
   if (smem > 48 * 1024) {                // the most any call needs, so that concurrent first calls agree
     static std::atomic<int> have[64];
     const cudaError_t e = allow_smem(kv_assign_kernel, (size_t)(4 * kMaxSeqs + 3) * sizeof(int), have);
