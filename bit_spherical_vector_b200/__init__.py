@@ -131,9 +131,14 @@ def _ptr(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(dtype) -> int:
-    import torch
-    return {torch.float16: SVQ_F16, torch.bfloat16: SVQ_BF16, torch.float32: SVQ_F32}[dtype]
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float16: SVQ_F16, torch.bfloat16: SVQ_BF16, torch.float32: SVQ_F32})
+    return _dtype_codes[dtype]
 
 
 # ----------------------------------------------------------------------------- format
@@ -368,22 +373,18 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _opt(t):
-    return None if t is None else t.data_ptr()
+# The three calls below are made for every layer of every step, and a short one's kernel takes less time than
+# the host does; so their checks are written out, without helpers that would format a message or pack arguments
+# each time.
+def _wrong(what: str, why: str):
+    raise ValueError(f"{what}: {why}")
 
 
-def _arrays(what: str, dtype, dev: int, *tensors):
+def _arrays(what: str, dtype, dev: int, tensors):
     """Contiguous arrays of one type on the current device (None: an optional one that is absent)."""
     for t in tensors:
         if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError(f"{what}: an array of {dtype} must be contiguous and on the current CUDA device")
-
-
-def _here(stream):
-    """The current device and the handle of the stream to use there."""
-    import torch
-    dev = torch._C._cuda_getDevice()
-    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+            _wrong(what, f"an array of {dtype} must be contiguous and on the current CUDA device")
 
 
 class KvCache:
@@ -439,18 +440,23 @@ def svq_kv_assign(lens, n_new, page_size: int, block_table, free_pages, n_free, 
     """Block table, positions and slots of one step from the requests' lengths: request b holds lens[b] tokens and
     gets n_new[b] (negative: it is done).  All int32 on the device; lens_out may be lens, n_free_out may be n_free."""
     import torch
-    what = "svq_kv_assign"
     n, rows = lens.numel(), slots.numel()
-    dev, st = _here(stream)
-    _arrays(what, torch.int32, dev, lens, n_new, block_table, free_pages, n_free, lens_out,
-            n_free_out, cu_rows, positions, slots)
-    _need(block_table.dim() == 2 and block_table.shape[0] == n and n_new.numel() == n and lens_out.numel() == n
-          and cu_rows.numel() == n + 1 and positions.numel() == rows and n_free.numel() == 1
-          and n_free_out.numel() == 1, f"{what}: sizes do not agree")
-    _check(lib().svq_kv_assign(lens.data_ptr(), n_new.data_ptr(), n, page_size, block_table.data_ptr(),
-                               block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), n_free.data_ptr(),
-                               lens_out.data_ptr(), n_free_out.data_ptr(), cu_rows.data_ptr(), positions.data_ptr(),
-                               slots.data_ptr(), rows, st), what)
+    dev = torch._C._cuda_getDevice()
+    _arrays("svq_kv_assign", torch.int32, dev, (lens, n_new, block_table, free_pages, n_free, lens_out, n_free_out,
+                                                cu_rows, positions, slots))
+    if block_table.dim() != 2:
+        _wrong("svq_kv_assign", "block_table must be [n_seqs][max_pages]")
+    n_table, width = block_table.shape
+    if not (n_table == n == n_new.numel() == lens_out.numel() == cu_rows.numel() - 1 and positions.numel() == rows
+            and n_free.numel() == 1 == n_free_out.numel()):
+        _wrong("svq_kv_assign", "sizes do not agree")
+    st = lib().svq_kv_assign(
+        lens.data_ptr(), n_new.data_ptr(), n, page_size, block_table.data_ptr(), width, free_pages.data_ptr(),
+        free_pages.numel(), n_free.data_ptr(), lens_out.data_ptr(), n_free_out.data_ptr(), cu_rows.data_ptr(),
+        positions.data_ptr(), slots.data_ptr(), rows,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise SvqError(st, "svq_kv_assign")
 
 
 def svq_qk_norm_rope_cache(q, k, v, q_gamma, k_gamma, eps: float, rope: Rope, positions, slots, cache: KvCache, q_out,
@@ -458,26 +464,29 @@ def svq_qk_norm_rope_cache(q, k, v, q_gamma, k_gamma, eps: float, rope: Rope, po
     """q [M][n_q * D], k and v [M][n_heads * D] (fp32, fp16 or bf16, rows any multiple of 8 apart) -> q_out
     [M][n_q][D] and the cache's slots; gammas fp16 [D] or None; rows with a negative slot are left out."""
     import torch
-    what = "svq_qk_norm_rope_cache"
-    D, wk = cache.head_dim, cache.n_heads * cache.head_dim
+    D, wk, x = cache.head_dim, cache.n_heads * cache.head_dim, q.dtype
     (M, wq), (Mk, wkk), (Mv, wkv), (Mo, heads, Do) = q.shape, k.shape, v.shape, q_out.shape
-    _need(Mk == Mv == Mo == M and wq == heads * D and wkk == wkv == wk and Do == D and positions.numel() == M
-          and slots.numel() == M and (q_gamma is None or q_gamma.numel() == D)
-          and (k_gamma is None or k_gamma.numel() == D), f"{what}: sizes do not agree")
+    if not (Mk == Mv == Mo == M == positions.numel() == slots.numel() and wq == heads * D and wkk == wkv == wk
+            and Do == D and (q_gamma is None or q_gamma.numel() == D) and (k_gamma is None or k_gamma.numel() == D)):
+        _wrong("svq_qk_norm_rope_cache", "sizes do not agree")
     (ldq, sq), (ldk, sk), (ldv, sv) = q.stride(), k.stride(), v.stride()
-    x = q.dtype
-    _need(k.dtype is x and v.dtype is x and (M == 0 or sq == sk == sv == 1), f"{what}: types or strides do not agree")
+    if k.dtype is not x or v.dtype is not x or (M and not sq == sk == sv == 1):
+        _wrong("svq_qk_norm_rope_cache", "types or strides do not agree")
     if M < 2:                                    # the distance between rows of one row says nothing
         ldq, ldk, ldv = wq, wk, wk
-    dev, st = _here(stream)
-    _need(q.get_device() == dev and k.get_device() == dev and v.get_device() == dev and rope.device == dev
-          and cache.device == dev, f"{what}: not on the current CUDA device")
-    _arrays(what, torch.int32, dev, positions, slots)
-    _arrays(what, torch.float16, dev, q_gamma, k_gamma)
-    _arrays(what, cache.dtype, dev, q_out)
-    _check(lib().svq_qk_norm_rope_cache(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(x), ldq, ldk, ldv, M,
-                                        heads, _opt(q_gamma), _opt(k_gamma), eps, rope._ref, positions.data_ptr(),
-                                        slots.data_ptr(), cache._ref, q_out.data_ptr(), st), what)
+    dev = torch._C._cuda_getDevice()
+    if not (q.get_device() == k.get_device() == v.get_device() == rope.device == cache.device == dev):
+        _wrong("svq_qk_norm_rope_cache", "not on the current CUDA device")
+    _arrays("svq_qk_norm_rope_cache", torch.int32, dev, (positions, slots))
+    _arrays("svq_qk_norm_rope_cache", torch.float16, dev, (q_gamma, k_gamma))
+    _arrays("svq_qk_norm_rope_cache", cache.dtype, dev, (q_out,))
+    st = lib().svq_qk_norm_rope_cache(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(x), ldq, ldk, ldv, M, heads,
+        None if q_gamma is None else q_gamma.data_ptr(), None if k_gamma is None else k_gamma.data_ptr(), eps, rope._ref,
+        positions.data_ptr(), slots.data_ptr(), cache._ref, q_out.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise SvqError(st, "svq_qk_norm_rope_cache")
 
 
 def svq_paged_attention_workspace_size(cache: KvCache, n_q_heads: int) -> int:
@@ -493,24 +502,31 @@ def svq_paged_attention(q, cache: KvCache, lens, block_table, scale: float, out,
     (row b, or row cu_rows[b + 1] - 1).  order (int32 [n_q * D]): column of each entry, the inverse of the o
     matrix's perm for its stored order; lse: fp32 [rows][n_q] or None.  ws: zero-filled once by svq_workspace_init."""
     import torch
-    what = "svq_paged_attention"
     rows, heads, D = q.shape
     n = lens.numel()
-    _need(D == cache.head_dim and out.shape == (rows, heads * D) and block_table.dim() == 2
-          and block_table.shape[0] == n and (cu_rows.numel() == n + 1 if cu_rows is not None else n <= rows)
-          and (order is None or order.numel() == heads * D) and (lse is None or lse.shape == (rows, heads)),
-          f"{what}: sizes do not agree")
-    dev, st = _here(stream)
-    _need(cache.device == dev, f"{what}: not on the current CUDA device")
-    _arrays(what, cache.dtype, dev, q)
-    _arrays(what, out.dtype, dev, out)
-    _arrays(what, torch.int32, dev, lens, block_table, cu_rows, order)
-    _arrays(what, torch.float32, dev, lse)
-    _arrays(what, ws.dtype, dev, ws)
-    _check(lib().svq_paged_attention(q.data_ptr(), rows, heads, cache._ref, lens.data_ptr(), _opt(cu_rows), n,
-                                     block_table.data_ptr(), block_table.shape[1], scale, _opt(order),
-                                     out.data_ptr(), _dtype_code(out.dtype), _opt(lse), ws.data_ptr(),
-                                     ws.numel() * ws.element_size(), st), what)
+    if block_table.dim() != 2:
+        _wrong("svq_paged_attention", "block_table must be [n_seqs][max_pages]")
+    n_table, width = block_table.shape
+    if not (D == cache.head_dim and out.shape == (rows, heads * D) and n_table == n
+            and (cu_rows.numel() == n + 1 if cu_rows is not None else n <= rows)
+            and (order is None or order.numel() == heads * D) and (lse is None or lse.shape == (rows, heads))):
+        _wrong("svq_paged_attention", "sizes do not agree")
+    dev = torch._C._cuda_getDevice()
+    if cache.device != dev:
+        _wrong("svq_paged_attention", "not on the current CUDA device")
+    _arrays("svq_paged_attention", torch.int32, dev, (lens, block_table, cu_rows, order))
+    _arrays("svq_paged_attention", cache.dtype, dev, (q,))
+    _arrays("svq_paged_attention", out.dtype, dev, (out,))
+    _arrays("svq_paged_attention", ws.dtype, dev, (ws,))
+    if lse is not None:
+        _arrays("svq_paged_attention", torch.float32, dev, (lse,))
+    st = lib().svq_paged_attention(
+        q.data_ptr(), rows, heads, cache._ref, lens.data_ptr(), None if cu_rows is None else cu_rows.data_ptr(), n,
+        block_table.data_ptr(), width, scale, None if order is None else order.data_ptr(), out.data_ptr(),
+        _dtype_code(out.dtype), None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes,
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise SvqError(st, "svq_paged_attention")
 
 
 # ------------------------------------------------------------------ calibration (ESG, radius grid, encoder, ABS)
