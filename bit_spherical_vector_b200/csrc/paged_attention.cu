@@ -90,18 +90,18 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 template <bool BF16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (BF16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -360,14 +360,19 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       // tile i is used, tile i + kStages - 1 goes into the stage that tile i - 1 has left
       cp_wait<S::kStages - 2>();
       __syncwarp();
-      const int next = i + S::kStages - 1;
-      if (next < todo) {
-        if ((next & 31) == 0) look_up(next);
-        load_tile(next, put_stage);
+      auto load_next = [&]() {
+        const int next = i + S::kStages - 1;
+        if (next < todo) {
+          if ((next & 31) == 0) look_up(next);
+          load_tile(next, put_stage);
+        }
+        cp_commit();
+        put_stage = put_stage + 1 == S::kStages ? 0 : put_stage + 1;
+      };
+      if (i < 0) {
+        load_next();
+        continue;
       }
-      cp_commit();
-      put_stage = put_stage + 1 == S::kStages ? 0 : put_stage + 1;
-      if (i < 0) continue;
       const int2 nb = note[warp][use];
       const uint32_t okm = (uint32_t)nb.x & 0xFFFFu;
       const int unit = nb.y;
@@ -411,19 +416,27 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
       }
 
       // scores of 16 keys: rows g8 and g8 + 8, query heads t2 and t2 + 1
-      float sc[NQ][4];
+      // two chains of products, half as long, where registers allow
+      constexpr bool kTwo = D < 256;
+      float sc[NQ][4], sd[NQ][4];
 #pragma unroll
       for (int q = 0; q < NQ; ++q)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[q][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[q][e] = sd[q][e] = 0.f;
       const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t a[4];
         ldsm4(kt + lrow * S::kRow + (((2 * ks + (lane >> 4)) ^ (lane & 7)) << 4), a);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) mma<BF16>(sc[q], a, qf[ks][q][0], qf[ks][q][1]);
+        for (int q = 0; q < NQ; ++q) mma<BF16>(kTwo && (ks & 1) ? sd[q] : sc[q], a, qf[ks][q][0], qf[ks][q][1]);
       }
+      load_next();                                         // issued while the products are on their way
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (kTwo) sc[q][e] += sd[q][e];
       const bool ok0 = (okm >> g8) & 1, ok1 = (okm >> (g8 + 8)) & 1;
       uint32_t ph[NQ][2], pl[NQ][2];
 #pragma unroll
