@@ -207,17 +207,50 @@ __global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_consta
     for (int k = 0; k < kBatch; ++k)
       if (k0 + k * gn < need_all) p.table[at[k]] = page[k];
   }
-  // released pages that the step does not take go onto the list
-  for (int i0 = n_free + g; i0 < itop - need_all; i0 += kBatch * gn) {
-    int page[kBatch];
+  // Released pages that the step does not take go onto the list, entry by entry where
+  // they are few.  Where every warp has kRun * 32 of them they mostly lie in long
+  // runs, the rows of done requests: a warp looks up the two runs that its next kRun
+  // * 32 begin in, takes what lies there with kRun loads a lane on their way (from an
+  // index held inside the runs: a load behind a condition would wait for the one
+  // before), and goes entry by entry from the third run on (1024 requests of up to 16384
+  // pages of one token, a tenth of them done: 271 -> 46 us).
+  // (Unsigned: they can be close to 2^31, and the last step of a loop passes that.)
+  const unsigned kept = max(itop - need_all - n_free, 0);
+  auto keep = [&](unsigned from, unsigned to, unsigned step) {
+    for (unsigned i0 = from; i0 < to; i0 += kBatch * step) {
+      int page[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * gn;
-      page[k] = i < itop - need_all ? stack.released(i - n_free) : 0;
+      for (int k = 0; k < kBatch; ++k) page[k] = i0 + k * step < to ? stack.released((int)(i0 + k * step)) : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (i0 + k * step < to) p.free_pages[n_free + i0 + k * step] = page[k];
+    }
+  };
+  constexpr unsigned kRun = 16;
+  if (kept < kRun * gn) {
+    keep(g, kept, gn);
+    return;
+  }
+  for (unsigned i0 = g / 32 * (kRun * 32); i0 < kept; i0 += kRun * gn) {
+    const unsigned to = min(kept, i0 + kRun * 32);
+    const int b0 = find_segment(gone, n, (int)i0);
+    const unsigned end0 = gone[b0 + 1];
+    const int b1 = end0 < to ? find_segment(gone, n, (int)end0) : b0;
+    const unsigned end = min(to, (unsigned)gone[b1 + 1]);
+    const int* row0 = p.table + (size_t)b0 * p.width - gone[b0];
+    const int* row1 = p.table + (size_t)b1 * p.width - gone[b1];
+    int page[kRun];
+#pragma unroll
+    for (unsigned k = 0; k < kRun; ++k) {
+      const unsigned i = min(i0 + k * 32 + lane, end - 1);
+      page[k] = (i < end0 ? row0 : row1)[i];
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (i0 + k * gn < itop - need_all) p.free_pages[i0 + k * gn] = page[k];
+    for (unsigned k = 0; k < kRun; ++k) {
+      const unsigned i = i0 + k * 32 + lane;
+      if (i < end) p.free_pages[n_free + i] = page[k];
+    }
+    keep(end + lane, to, 32);
   }
 }
 

@@ -71,6 +71,44 @@ def test_against_oracle(n, page, longest, rows, in_place):
     assert svq.svq_get_device_status() == svq.SVQ_OK
 
 
+# rows of done requests that are kept free: many short ones, a few long ones, long ones between short ones
+@pytest.mark.parametrize("n,longest,rows", [(4096, 90, 100), (40, 9000, 50), (3000, 250, 16000), (7, 60000, 9000)])
+@pytest.mark.parametrize("mixed", [False, True])
+def test_long_releases(n, longest, rows, mixed):
+    need_gpu()
+    rng = np.random.default_rng(n + longest)
+    lens, new, table, free, n_free = scene(rng, n, 1, longest, rows, done=0.6, spare=11)
+    new[n // 2] = -1                                         # one done request at least, in the middle
+    if mixed:
+        short = rng.random(n) < 0.5
+        lens[short] = np.minimum(lens[short], rng.integers(0, 3, short.sum()))
+    want = oa.kv_assign(lens, new, 1, table, free, n_free, rows)
+    assert want is not None
+    for in_place in (False, True):
+        same(call(lens, new, 1, table, free, n_free, rows, in_place), want)
+    assert svq.svq_get_device_status() == svq.SVQ_OK
+
+
+@pytest.mark.parametrize("last", [-1, 1, 0])
+def test_long_releases_on_one_cta(last):
+    need_gpu()
+    rng = np.random.default_rng(3)
+    lens, new = np.array([1000, 1, 0, 1000, 513, 999, 700, 1000, 900]), np.full(9, -1)
+    new[-1] = last
+    table = np.full((9, 910), -1)
+    lens = np.minimum(lens, 910)
+    deal = rng.permutation(int(lens.sum()) + 4)
+    at = 0
+    for b, l in enumerate(lens):
+        table[b, :l] = deal[at:at + l]
+        at += l
+    free = np.concatenate([deal[at:], np.full(at, -7)])
+    want = oa.kv_assign(lens, new, 1, table, free, 4, 5)
+    assert want is not None and want["n_free_out"] > 4100
+    same(call(lens, new, 1, table, free, 4, 5), want)
+    assert svq.svq_get_device_status() == svq.SVQ_OK
+
+
 @pytest.mark.parametrize("rows", [64, 9000])                 # one CTA and a cluster of them
 @pytest.mark.parametrize("what", ["negative", "too long", "too many rows", "no pages", "free count", "huge"])
 def test_refused_steps_change_nothing(what, rows):
