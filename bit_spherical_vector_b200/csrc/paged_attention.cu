@@ -33,6 +33,11 @@
 // the loop, the CTAs' parts through the workspace by the CTA that arrives last
 // (a counter per CTA that wraps back to zero), in CTA order, so results do not
 // depend on timing.  Nothing waits on another CTA.
+//
+// B200, in a CUDA graph, heads of 128, 4 query heads to a key head, 8 key heads: one
+// request of 131072 keys 87 us = 6.2 TB/s (7.1 in the loop; the front takes 2.6 us, the
+// joins 5), 128 requests of up to 4096 keys 184 us = 6.1 TB/s, both bound by HBM (copy
+// rate 6.6); one of 512 keys 8 us, a chain of dependent loads and one join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -10,7 +10,7 @@
 // The angle is what needs care: at position 10^6 an fp32 product is off by
 // 0.03 rad.  It is formed in turns in fp64 (position * (inv_freq / 2 pi)), the
 // whole turns are dropped there, and only the remaining half turn goes to fp32
-// (sincospi): off by 2e-7 at any position an int32 holds up to 10^8.
+// (sincospi): off by 2.4e-7 at the largest int32 position, by rounding alone near 0.
 //
 // One read of q|k|v and one write of q, k and v bounds long calls in principle,
 // latency short ones.  A warp takes heads of one kind (queries, keys or values) of
@@ -20,6 +20,12 @@
 // The sines are formed once for the warp's heads, a share by each of the 256 / D
 // lanes that need the same ones, and multiplied with gamma.  Nothing else is
 // exchanged but the sum of squares, and warps do not wait for one another.
+// (A CTA per row with the sines in shared memory: 16.5 us where this took 13.6,
+// 2.1 us for one row against 1.5.)
+//
+// B200, in a CUDA graph: 2048 rows of 32 + 8 + 8 heads of 128, bf16, 12.8 us =
+// 3.9 TB/s (copy rate 6.6), bound by instruction issue; 777 rows of 14 + 2 + 2
+// heads of 64 3.2 us, one row 1.7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -2,11 +2,11 @@
 
 Bar for each entry: half a step of the output type at the exact value (plus half a subnormal step) and 2e-6 of
 factor times the length of the entry's pair.  Where the 2e-6 comes from, in units of u = 2^-24: the mean of
-squares is a chain of at most 8 fused additions per lane and 5 in the butterfly (13 u, halved by the root), the
-root, the reciprocal and the two products add 4 u: 10.5 u.  The angle is exact to 3 u pi (its rounding to fp32 in
-turns: at most 2^-26 turns), sincospi adds 2 ulp (4 u): cosine and sine are off by at most 13.5 u each, which
-turns the pair by sqrt(2) * 13.5 u = 19 u of its length; their products with factor, the two products and the sum
-add 4 u.  Together 34 u < 2.1e-6; the bar adds the halves of fp64's own sums."""
+squares is a chain of at most 5 fused additions per lane and 5 in the butterfly (10 u; the product with 1/D
+is exact) and eps one more, halved by the root: 5.5 u.  The reciprocal root adds 1 u; gamma, factor, the two
+products and the sum 5 u.  The angle is exact to 3 u pi (its rounding to fp32 in turns: at most 2^-26 turns), sincospi adds 2 ulp (4 u):
+cosine and sine are off by at most 13.5 u each, which turns the pair by sqrt(2) * 13.5 u = 19 u of its length.
+Together 30.5 u; the bar of 34 u leaves the rest to the second-order terms."""
 import numpy as np
 import pytest
 
