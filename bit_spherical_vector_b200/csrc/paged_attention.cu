@@ -130,9 +130,25 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// One instruction that makes a pair of floats NaN if one of four numbers is (also, for
+// nothing, where their products run over).
+__device__ __forceinline__ void probe_nan(unsigned long long& probe, const float (&v)[4]) {
+  unsigned long long a, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(v[0]), "f"(v[1]));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(v[2]), "f"(v[3]));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(probe) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ bool is_nan(unsigned long long probe) {
+  const float s = __uint_as_float((uint32_t)probe) + __uint_as_float((uint32_t)(probe >> 32));
+  return s != s;
+}
 // Weight of a part with maximum m in a join whose maximum is M (both in units of
-// log2): a part that saw no key has m = -inf and weight 0.
-__device__ __forceinline__ float part_weight(float m, float M) { return m == kNegInf ? 0.f : ex2(m - M); }
+// log2): a part that saw no key has m = -inf and weight 0.  Any other weighs the least
+// positive number at least, which adds nothing to a finite sum (3e38 * 2^-149 is 5e-7 of
+// a result of that size's smallest step) and leaves an infinite one infinite.
+__device__ __forceinline__ float part_weight(float m, float M) {
+  return m == kNegInf ? 0.f : fmaxf(ex2(m - M), 1.401298464e-45f);
+}
 
 // Where a unit's result goes: row of the output, first query head << 8 | heads,
 // and the CTAs that share the unit.
@@ -145,6 +161,143 @@ __device__ __forceinline__ void weigh(float4& acc, float f, const float4& v) {
   acc.y = fmaf(v.y, f, acc.y);
   acc.z = fmaf(v.z, f, acc.z);
   acc.w = fmaf(v.w, f, acc.w);
+}
+
+// An infinite value that counts.  A weight is multiplied in two terms, of which one may be
+// 0 or negative, so the products make NaN of a sum that is infinite.  A warp that has met
+// NaN among its sums goes through its range [w0, w1) of the line once more: weights of
+// finite scores are positive, so infinite values of one sign give that infinity; both
+// signs, a NaN or an infinity whose score is -inf (0 times infinity) give NaN, and so does
+// a score that is NaN or +inf (then all of a row is NaN).  Sums are found where the loop
+// has left them: parts in `part0` or `part1` (slots 0 and 1), Pitch apart, whole units in
+// the output.  The values of a unit with NaN are read once more for all its rows, a lane
+// D / 32 entries of a key (128 requests of up to 4096 keys, an infinity in each: 0.8 ms).
+// Calls without infinities and NaN never come here; what they pay is the look at the sums
+// where a warp leaves a unit, D / 16 instructions for each 8 heads: 0.1 to 0.2 us of short
+// calls (1 request of 3 keys: 4.1 -> 4.2 us), nothing of long ones but with thousands of
+// short units of wide heads (245 requests of 186 keys, 96 heads of 256 on 8: 134 -> 138 us).
+template <int D, int R, int Pitch, bool BF16>
+__device__ __noinline__ void mend_sums(const PagedAttnParams& p, const int* pre, float* part0, float* part1, long long w0,
+                                       long long w1) {
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;      // infinity: larger magnitudes are NaN
+  constexpr int E = D / 32;                                // entries of a lane
+  constexpr uint32_t kAll = (1u << E) - 1u;
+  const AttnSeqs seqs{pre, reinterpret_cast<const uint32_t*>(pre + p.n_seqs + 1)};
+  const uint32_t out_inf = p.out_bf16 ? 0x7F80u : 0x7C00u;
+  const int lane = threadIdx.x & 31, heads = p.kv.n_heads * p.row_tiles;
+  __syncwarp();                                            // the sums are written
+  for (long long g = w0; g < w1;) {
+    AttnCursor c;
+    c.set(seqs, p.n_seqs, heads, p.by_heads, g);
+    const long long end = min(w1, g + c.nt - c.t);
+    const bool whole = c.t == 0 && end == g + c.nt;
+    float* part = (end == w1 ? part1 : part0) + lane * E;
+    const int j0 = c.t * kTile, j1 = min(seqs.len(c.b), (c.t + (int)(end - g)) * kTile);
+    g = end;
+    const int kv_head = p.by_row_tiles.div(c.h), rt = c.h - kv_head * p.row_tiles, count = min(R, p.group - rt * R);
+    const int64_t at_row = ((int64_t)seqs.row(c.b) * p.n_q + kv_head * p.group + rt * R) * D;
+    const uint16_t* q = p.q + at_row;
+    uint16_t* out = p.out + at_row + lane * E;
+    auto nans = [&](int r) {                               // the lane's entries of row r that are NaN
+      uint32_t m = 0;
+      for (int e = 0; e < E; ++e) {
+        const bool nan = whole ? (__ldcg(out + r * D + e) & 0x7FFFu) > out_inf : part[r * Pitch + e] != part[r * Pitch + e];
+        m |= (uint32_t)nan << e;
+      }
+      return m;
+    };
+    auto place_of = [&](int j) -> int64_t {                // of a key's first entry, -1: none that counts
+      if (j >= j1) return -1;
+      const int jp = p.by_page.div(j), page = p.table[(int64_t)c.b * p.width + jp];
+      if ((unsigned)page >= (unsigned)p.kv.n_pages) return -1;
+      return (int64_t)page * p.kv.page_stride + (int64_t)(j - jp * p.kv.page_size) * p.kv.token_stride +
+             (int64_t)kv_head * p.kv.head_stride;
+    };
+    bool any = false;
+    for (int r = 0; r < count; ++r) any |= nans(r) != 0;
+    if (!__any_sync(0xFFFFFFFFu, any)) continue;
+
+    uint32_t up = 0, down = 0, nan = 0, zero[R];           // bit e: what the values of the lane's entry hold
+#pragma unroll
+    for (int r = 0; r < R; ++r) zero[r] = 0;               // an infinity without weight in row r
+    for (int j = j0; j < j1 && !__all_sync(0xFFFFFFFFu, nan == kAll); j += 32) {
+      const int64_t mine = place_of(j + lane);
+      constexpr int kBatch = 8;
+#pragma unroll 1
+      for (int x0 = 0; x0 < 32; x0 += kBatch) {
+        uint32_t w[kBatch][E / 2];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, x0 + x);
+          const uint32_t* v = reinterpret_cast<const uint32_t*>(p.kv.v + (at < 0 ? 0 : at) + lane * E);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) w[x][e] = at < 0 ? 0u : v[e];
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          uint32_t here = 0;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const uint32_t v = w[x][e >> 1] >> (16 * (e & 1)) & 0xFFFFu, bit = 1u << e;
+            if ((v & 0x7FFFu) > kInf) nan |= bit;
+            if ((v & 0x7FFFu) != kInf) continue;
+            here |= bit;
+            (v & 0x8000u ? down : up) |= bit;
+          }
+          if (!__any_sync(0xFFFFFFFFu, here != 0)) continue;
+          const uint16_t* k = p.kv.k + __shfl_sync(0xFFFFFFFFu, mine, x0 + x);
+#pragma unroll 1
+          for (int r = 0; r < count; ++r) {
+            float s = 0.f;
+            for (int e = lane * 2; e < D; e += 64) {
+              const float2 a = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(q + r * D + e));
+              const float2 b = unpack2<BF16>(*reinterpret_cast<const uint32_t*>(k + e));
+              s = fmaf(a.x, b.x, fmaf(a.y, b.y, s));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if (s * p.scale_log2 != kNegInf) continue;
+#pragma unroll
+            for (int i = 0; i < R; ++i) zero[i] |= i == r ? here : 0u;
+          }
+        }
+      }
+    }
+#pragma unroll 1
+    for (int r = 0; r < count; ++r) {
+      const uint32_t have = nans(r);
+      uint32_t fix = have & ~nan & (up ^ down);
+#pragma unroll
+      for (int i = 0; i < R; ++i) fix &= i == r ? ~zero[i] : ~0u;
+      if (!__any_sync(0xFFFFFFFFu, fix != 0)) continue;
+      if (__all_sync(0xFFFFFFFFu, have == kAll)) {         // all of a row: its scores may be the reason
+        bool lost = false;
+        for (int j = j0; j < j1 && !__any_sync(0xFFFFFFFFu, lost); j += 32) {
+          const int64_t at = place_of(j + lane);
+          float s = 0.f;
+          for (int e = 0; e < D && at >= 0; e += 8) {
+            const uint4 a4 = *reinterpret_cast<const uint4*>(q + r * D + e);
+            const uint4 b4 = *reinterpret_cast<const uint4*>(p.kv.k + at + e);
+            const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 u = unpack2<BF16>(a[i]), t = unpack2<BF16>(b[i]);
+              s = fmaf(u.x, t.x, fmaf(u.y, t.y, s));
+            }
+          }
+          lost = !(s * p.scale_log2 < -kNegInf);
+        }
+        if (__any_sync(0xFFFFFFFFu, lost)) continue;
+      }
+      for (int e = 0; e < E; ++e) {
+        if (!((fix >> e) & 1)) continue;
+        const bool plus = (up >> e) & 1;
+        if (whole) out[r * D + e] = (uint16_t)(out_inf | (plus ? 0u : 0x8000u));
+        else part[r * Pitch + e] = plus ? -kNegInf : kNegInf;
+      }
+    }
+  }
+  __syncwarp();
 }
 
 template <int D, int NQ, bool BF16>
@@ -166,6 +319,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   __shared__ int part_unit[P];                                     // unit of a part, -1: none
   __shared__ int2 note[W][S::kStages];                             // tile in a stage: keys that count and flags; unit
   __shared__ int2 wsum[W];
+  __shared__ bool spoilt[W];                                       // NaN among the warp's sums
   __shared__ bool joined[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = p.n_seqs, heads = p.kv.n_heads * p.row_tiles;
@@ -260,6 +414,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   const uint32_t ring = sm100::smem_u32(smem) + warp * S::kStages * S::kStage;
   const int g8 = lane >> 2, t2 = (lane & 3) * 2;
   if (lane < 2) part_unit[2 * warp + lane] = -1;
+  if (lane == 0) spoilt[warp] = false;
 
   auto log_sum = [](float m, float l) {
     return l == 0.f ? kNegInf : fmaf(m - kShift, 0.6931471805599453f, logf(l));
@@ -507,6 +662,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
           ls[q][0] += __shfl_xor_sync(0xFFFFFFFFu, ls[q][0], x);
           ls[q][1] += __shfl_xor_sync(0xFFFFFFFFu, ls[q][1], x);
         }
+      unsigned long long probe = 0;                        // two floats, NaN if a sum is
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) probe_nan(probe, o[ks][q]);
+      if (is_nan(probe)) spoilt[warp] = true;
       if (!(unit_ends && from_start)) {
         // A part: in mid-range (the ring is in use) to the workspace, else to the
         // ring, which is drained: every tile of the range has been waited for.
@@ -560,7 +721,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncwarp();
-  if (part_unit[2 * warp] >= 0) {
+  const bool parked = part_unit[2 * warp] >= 0, nan_met = spoilt[warp];
+  if (nan_met) mend_sums<D, R, kPitch, BF16>(p, pre, spilled, part_room(warp, 1), w0, w1);
+  if (parked) {
     const float4* src = reinterpret_cast<const float4*>(spilled);
     float4* dst = reinterpret_cast<float4*>(part_room(warp, 0));
 #pragma unroll 8

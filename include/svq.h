@@ -466,6 +466,8 @@ SVQ_API int svq_qk_norm_rope_cache(const void* q, const void* k, const void* v, 
  *   s_j = scale * q . k_j,  p = softmax(s),  o = sum_j p_j v_j
  * (scores and sums fp32, the softmax weights carried in two terms of the cache's
  * type, o rounded once).  n_q_heads a multiple of n_heads, at most 1024.
+ * Infinite values count as in the formula: an entry with v_j of one infinity is that
+ * infinity however small p_j is, with both signs NaN, and NaN where s_j is -inf.
  * Rows: with cu_rows NULL request b is row b of q, out and lse; with cu_rows
  * [n_seqs + 1] (svq_kv_assign's) it is row cu_rows[b + 1] - 1, its last row of the
  * step, and a request without a row is left out.  Other rows of out and lse are
