@@ -216,12 +216,21 @@ __global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_consta
   // before), and goes entry by entry from the third run on (1024 requests of up to 16384
   // pages of one token, a tenth of them done: 271 -> 46 us).
   // (Unsigned: they can be close to 2^31, and the last step of a loop passes that.)
+  // A page outside the pool goes onto the list like any other, and is reported here: the
+  // step that takes it may be far (`worst` is looked at once: a branch at every store made
+  // long releases half as slow again).
   const unsigned kept = max(itop - need_all - n_free, 0);
+  unsigned worst = 0;
+  auto report = [&] {
+    if (worst >= (unsigned)p.n_pages) *p.status = SVQ_ERR_INVALID_ARG;
+  };
   auto keep = [&](unsigned from, unsigned to, unsigned step) {
     for (unsigned i0 = from; i0 < to; i0 += kBatch * step) {
       int page[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) page[k] = i0 + k * step < to ? stack.released((int)(i0 + k * step)) : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) worst = max(worst, (unsigned)page[k]);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (i0 + k * step < to) p.free_pages[n_free + i0 + k * step] = page[k];
@@ -230,6 +239,7 @@ __global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_consta
   constexpr unsigned kRun = 16;
   if (kept < kRun * gn) {
     keep(g, kept, gn);
+    report();
     return;
   }
   for (unsigned i0 = g / 32 * (kRun * 32); i0 < kept; i0 += kRun * gn) {
@@ -247,12 +257,15 @@ __global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_consta
       page[k] = (i < end0 ? row0 : row1)[i];
     }
 #pragma unroll
+    for (unsigned k = 0; k < kRun; ++k) worst = max(worst, (unsigned)page[k]);
+#pragma unroll
     for (unsigned k = 0; k < kRun; ++k) {
       const unsigned i = i0 + k * 32 + lane;
       if (i < end) p.free_pages[n_free + i] = page[k];
     }
     keep(end + lane, to, 32);
   }
+  report();
 }
 
 }  // namespace

@@ -396,7 +396,8 @@ typedef struct svq_kv_cache {
  * lies outside 0..n_pages, then lens_out = lens, *n_free_out = *n_free, cu_rows
  * = 0 and all rows -1, nothing else is written, and the device status word is set to
  * SVQ_ERR_INVALID_ARG.  A page number outside 0..n_pages-1 in the table or the
- * list gives slot -1 and sets the status word.  n_pages * page_size, max_pages *
+ * list that the step looks at sets the status word: a row of it gets slot -1, and a
+ * released one goes onto the list as it is.  n_pages * page_size, max_pages *
  * page_size and n_seqs * max_pages < 2^31, max_rows <= 2^30.
  * But for the two named pairs no array may overlap another.
  */
