@@ -459,7 +459,8 @@ int svq_rope_frequencies(int rot_dim, double base, int scaling, double scale, in
     };
     const double lo = std::fmax(std::floor(at(32.0)), 0.0), hi = std::fmin(std::ceil(at(1.0)), rot_dim - 1.0);
     for (int i = 0; i < half; ++i) {
-      const double ramp = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
+      // (the ramp's ends lie inside the head, so over a few positions its upper one would be below pair 0)
+      const double ramp = i >= at(1.0) ? 1.0 : std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 0.001), 0.0), 1.0);
       inv_freq[i] = inv_freq[i] / scale * ramp + inv_freq[i] * (1.0 - ramp);
     }
     *factor = (float)(0.1 * std::log(scale) + 1.0);
