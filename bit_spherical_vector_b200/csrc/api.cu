@@ -545,7 +545,8 @@ int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_
   const int st = check_cache(cache);
   if (st != SVQ_OK) return st;
   if (out_dtype != SVQ_F16 && out_dtype != SVQ_BF16) return SVQ_ERR_INVALID_ARG;
-  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return SVQ_ERR_INVALID_ARG;      // rejects NaN and infinities
+  const float scale_log2 = scale * 1.4426950408889634f;    // the kernel's scores are in units of log2
+  if (!(scale_log2 >= -3.0e38f && scale_log2 <= 3.0e38f)) return SVQ_ERR_INVALID_ARG;      // rejects NaN and infinities
   if (n_seqs < 0 || n_rows < 0 || max_pages < 1) return SVQ_ERR_INVALID_ARG;
   // the tiles of all requests are counted in 32 bits
   if (n_seqs > svq::kMaxSeqs || n_rows > (1 << 26) || (int64_t)max_pages * cache->page_size > INT32_MAX - 16 ||
@@ -575,7 +576,7 @@ int svq_paged_attention(const uint16_t* q, int n_rows, int n_q_heads, const svq_
   p.cta_part = reinterpret_cast<float*>(w + plan.cta_part);
   p.warp_part = reinterpret_cast<float*>(w + plan.warp_part);
   p.kv = view_of(*cache);
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale_log2;
   p.n_seqs = n_seqs; p.width = max_pages; p.n_q = n_q_heads; p.n_rows = n_rows;
   p.group = n_q_heads / cache->n_heads;
   p.row_tiles = (p.group + plan.rows - 1) / plan.rows;

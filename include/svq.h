@@ -486,9 +486,9 @@ SVQ_API int svq_qk_norm_rope_cache(const void* q, const void* k, const void* v, 
  * outside 0..max_pages * page_size is clamped, a row outside 0..n_rows-1 is left
  * out, a key on a page outside the pool does not count, an entry that order sends
  * outside the row is dropped; each sets the device status word to SVQ_ERR_INVALID_ARG.
- * n_seqs <= 4096, max_pages * page_size < 2^31 - 16 and n_seqs * (max_pages *
- * page_size / 16 + 1) < 2^31.  out, lse and the workspace must not overlap the
- * inputs or each other.
+ * |scale| <= 2e38, n_seqs <= 4096, max_pages * page_size < 2^31 - 16 and
+ * n_seqs * (max_pages * page_size / 16 + 1) < 2^31.  out, lse and the workspace must
+ * not overlap the inputs or each other.
  * Workspace (svq_paged_attention_workspace_size; the lengths and n_seqs do not
  * matter): completion counters in its first 64 KiB, zero before the first call
  * (svq_workspace_init), left zero by every completed call, then parts of split
