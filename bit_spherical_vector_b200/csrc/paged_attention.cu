@@ -416,8 +416,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   if (lane < 2) part_unit[2 * warp + lane] = -1;
   if (lane == 0) spoilt[warp] = false;
 
+  // (the sum without the shift, which is exact: m - kShift would round a small m to the size of 15)
   auto log_sum = [](float m, float l) {
-    return l == 0.f ? kNegInf : fmaf(m - kShift, 0.6931471805599453f, logf(l));
+    return l == 0.f ? kNegInf : fmaf(m, 0.6931471805599453f, logf(l * (BF16 ? 1.f : 0x1p-15f)));
   };
   auto put4 = [&](int64_t row, int head, int d, float2 ml, const float4& acc) {
     const float inv = ml.y == 0.f ? 0.f : 1.f / ml.y;
