@@ -421,7 +421,8 @@ SVQ_API int svq_kv_assign(const int32_t* lens, const int32_t* n_new, int n_seqs,
  *   SVQ_ROPE_YARN    theta_i below 1 turn over trained_len divided by scale, above
  *                    32 turns unchanged, a linear ramp over the pair index between,
  *                    and factor = 0.1 ln(scale) + 1 (YaRN, arXiv 2309.00071)
- * base > 1, scale >= 1 (ignored by SVQ_ROPE_PLAIN), trained_len >= 1 (SVQ_ROPE_YARN).
+ * 1 < base <= 1e300, 1 <= scale <= 1e6 (ignored by SVQ_ROPE_PLAIN), trained_len >= 1
+ * (SVQ_ROPE_YARN; the ramp's ends are pair indices rounded outwards, within the head).
  */
 typedef struct svq_rope {
   const double* inv_freq; /* device, 8-byte aligned */
@@ -449,10 +450,12 @@ SVQ_API int svq_rope_frequencies(int rot_dim, double base, int scaling, double s
  * q [M][n_q_heads * head_dim], k and v [M][n_heads * head_dim] of x_dtype (SVQ_F32,
  * SVQ_F16 or SVQ_BF16), 16-byte aligned, rows ldq, ldk, ldv elements apart
  * (multiples of 8; three views of one fused output are fine); gammas fp16
- * [head_dim], 16-byte aligned; q_out 16-byte aligned.  The angle is reduced in
- * fp64: its error is below 1e-6 at any position below 10^8.  0 <= M <= 2^20,
- * n_q_heads <= 1024.  Tolerance used by the tests: half a step of the output type
- * plus 8e-6 of the pair's magnitude.
+ * [head_dim], 16-byte aligned; q_out 16-byte aligned.  q_out may be q itself where
+ * x_dtype is the cache's type and ldq = n_q_heads * head_dim; else neither q_out nor
+ * the cache may overlap an input.  The angle is reduced in fp64: its error is below
+ * 1e-6 at any position below 10^8.  0 <= M <= 2^20, n_q_heads <= 1024.  Tolerance
+ * used by the tests: half a step of the output type plus 34 * 2^-24 (2.0e-6) of the
+ * pair's magnitude.
  */
 SVQ_API int svq_qk_norm_rope_cache(const void* q, const void* k, const void* v, int x_dtype, int64_t ldq,
                                    int64_t ldk, int64_t ldv, int M, int n_q_heads, const uint16_t* q_gamma,
