@@ -272,8 +272,8 @@ __global__ void __launch_bounds__(kThreads) kv_assign_kernel(const __grid_consta
 
 cudaError_t launch_kv_assign(const KvAssignParams& p, cudaStream_t st) {
   const size_t smem = (size_t)(4 * p.n_seqs + 3) * sizeof(int);
-  // One CTA where there is little to spread, which a cluster makes 0.2 us slower (16
-  // decode rows: 2.9 us against 3.1 us); a cluster where rows are many (543 requests
+  // One CTA where there is little to spread, which a cluster makes 0.3 us slower (16
+  // decode rows: 2.7 us against 3.0 us); a cluster where rows are many (543 requests
   // and 3339 rows: 4.8 us against 6.9 us) or the table is large, since a done request
   // may release a long row of it (63 requests of up to 3909 pages: 7.5 us against 30 us).
   const bool small = p.max_rows <= 2 * kThreads && (long long)p.n_seqs * p.width <= 8192;

@@ -3,9 +3,10 @@
 //
 //   s_j = scale * q . k_j,  p_j = e^(s_j - max s),  o = sum_j p_j v_j / sum_j p_j,   j < len
 //
-// Every key and value is read once for the whole group of query heads that
-// shares it, so the cache's bytes bound the call; everything here serves to keep
-// loads in flight on every SM whatever the lengths are.
+// Every key and value is read once for all query heads that share it, up to 16
+// (a larger group reads it again for each row tile of 16), so the cache's bytes bound
+// the call; everything here serves to keep loads in flight on every SM whatever the
+// lengths are.
 //
 // Split.  A unit is one (request, key head, row tile of at most 8 or 16 query
 // heads); its keys are cut into tiles of 16.  All tiles of the call, in (request,
@@ -144,8 +145,8 @@ __device__ __forceinline__ bool is_nan(unsigned long long probe) {
 }
 // Weight of a part with maximum m in a join whose maximum is M (both in units of
 // log2): a part that saw no key has m = -inf and weight 0.  Any other weighs the least
-// positive number at least, which adds nothing to a finite sum (3e38 * 2^-149 is 5e-7 of
-// a result of that size's smallest step) and leaves an infinite one infinite.
+// positive number at least: an infinite sum stays infinite, and to finite ones it adds
+// 2^-149 of the part's at most.
 __device__ __forceinline__ float part_weight(float m, float M) {
   return m == kNegInf ? 0.f : fmaxf(ex2(m - M), 1.401298464e-45f);
 }

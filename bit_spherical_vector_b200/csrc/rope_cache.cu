@@ -10,7 +10,8 @@
 // The angle is what needs care: at position 10^6 an fp32 product is off by
 // 0.03 rad.  It is formed in turns in fp64 (position * (inv_freq / 2 pi)), the
 // whole turns are dropped there, and only the remaining half turn goes to fp32
-// (sincospi): off by 2.4e-7 at the largest int32 position, by rounding alone near 0.
+// (sincospi): off by less than 5e-7 rad at the largest int32 position (the fp64 product
+// 4e-7, its rounding to fp32 1e-7), by the 1e-7 alone near 0.
 //
 // One read of q|k|v and one write of q, k and v bounds long calls in principle,
 // latency short ones.  A warp takes heads of one kind (queries, keys or values) of
@@ -23,9 +24,12 @@
 // (A CTA per row with the sines in shared memory: 16.5 us where this took 13.6,
 // 2.1 us for one row against 1.5.)
 //
-// B200, in a CUDA graph: 2048 rows of 32 + 8 + 8 heads of 128, bf16, 12.8 us =
-// 3.9 TB/s (copy rate 6.6), bound by instruction issue; 777 rows of 14 + 2 + 2
-// heads of 64 3.2 us, one row 1.7 us.
+// B200, in a CUDA graph: 2048 rows of 32 + 8 + 8 heads of 128, bf16, 12.9 us =
+// 3.9 TB/s (copy rate 6.6); 777 rows of 14 + 2 + 2 heads of 64 3.2 us, one row 1.5 us.
+// The 2048 rows are bound by latency on too few warps: 71 registers leave 28 warps an
+// SM, so their 8192 warps run in two waves, each through its own chain of slot,
+// position, sines and loads; schedulers issue in 57 % of the cycles, and HBM is at 59 %
+// of the copy rate.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -271,8 +275,12 @@ template <int D, int XT, bool BF16>
 cudaError_t launch_dx(RopeCacheParams p, int num_sms, cudaStream_t st) {
   // Few rows: a step per warp, so that latency is all there is.  Many: as many
   // steps as leave 48 warps for each SM (the sines of a row are formed anew in every
-  // warp), two, or four, eight or sixteen: whole turns of the loop (2048 rows of 48
-  // heads of 128: 12.9 us in eights, 14.2 us in sixes).
+  // warp), a power of two up to sixteen so that slices are mostly whole turns of the
+  // loop (2048 rows of 48 heads of 128: 12.9 us in eights, 14.2 us in sixes), and no
+  // more than the longest kind of head has (which may be odd).  48 is measured, not the
+  // warps that an SM holds: 28 takes those rows by sixteens, 17.5 us, though 64 rows of
+  // 64 + 8 + 8 heads of 256 gain (4.1 -> 3.4 us); 96 takes them by fours, 12.8 us, and 365
+  // rows of 20 + 4 + 4 heads of 256 lose (5.2 -> 6.0 us).
   constexpr int kHeads = 256 / D;
   const int q_steps = (p.n_q + kHeads - 1) / kHeads, kv_steps = (p.kv.n_heads + kHeads - 1) / kHeads;
   const long long all = (long long)p.M * (q_steps + 2 * kv_steps), warps = (long long)num_sms * 48;
