@@ -417,7 +417,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) paged_attn_kernel(const
   if (lane < 2) part_unit[2 * warp + lane] = -1;
   if (lane == 0) spoilt[warp] = false;
 
-  // (the sum without the shift, which is exact: m - kShift would round a small m to the size of 15)
+  // the shift is taken off the sum, which is exact; m - kShift would round a small m to the
+  // size of 15 (lse of 1, 2 and 4 keys off by 3.4, 2.2 and 1.5e-7 of itself, so by 1.9, 1.3
+  // and 0.9e-7)
   auto log_sum = [](float m, float l) {
     return l == 0.f ? kNegInf : fmaf(m, 0.6931471805599453f, logf(l * (BF16 ? 1.f : 0x1p-15f)));
   };
