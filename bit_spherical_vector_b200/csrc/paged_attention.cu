@@ -193,7 +193,8 @@ __device__ __noinline__ void mend_sums(const PagedAttnParams& p, const int* pre,
     const long long end = min(w1, g + c.nt - c.t);
     const bool whole = c.t == 0 && end == g + c.nt;
     float* part = (end == w1 ? part1 : part0) + lane * E;
-    const int j0 = c.t * kTile, j1 = min(seqs.len(c.b), (c.t + (int)(end - g)) * kTile);
+    // (unsigned: a loop's last step passes a length next to 2^31)
+    const unsigned j0 = c.t * kTile, j1 = min((unsigned)seqs.len(c.b), (c.t + (unsigned)(end - g)) * kTile);
     g = end;
     const int kv_head = p.by_row_tiles.div(c.h), rt = c.h - kv_head * p.row_tiles, count = min(R, p.group - rt * R);
     const int64_t at_row = ((int64_t)seqs.row(c.b) * p.n_q + kv_head * p.group + rt * R) * D;
@@ -207,11 +208,11 @@ __device__ __noinline__ void mend_sums(const PagedAttnParams& p, const int* pre,
       }
       return m;
     };
-    auto place_of = [&](int j) -> int64_t {                // of a key's first entry, -1: none that counts
+    auto place_of = [&](unsigned j) -> int64_t {           // of a key's first entry, -1: none that counts
       if (j >= j1) return -1;
-      const int jp = p.by_page.div(j), page = p.table[(int64_t)c.b * p.width + jp];
+      const int jp = p.by_page.div((int)j), page = p.table[(int64_t)c.b * p.width + jp];
       if ((unsigned)page >= (unsigned)p.kv.n_pages) return -1;
-      return (int64_t)page * p.kv.page_stride + (int64_t)(j - jp * p.kv.page_size) * p.kv.token_stride +
+      return (int64_t)page * p.kv.page_stride + (int64_t)((int)j - jp * p.kv.page_size) * p.kv.token_stride +
              (int64_t)kv_head * p.kv.head_stride;
     };
     bool any = false;
@@ -221,7 +222,7 @@ __device__ __noinline__ void mend_sums(const PagedAttnParams& p, const int* pre,
     uint32_t up = 0, down = 0, nan = 0, zero[R];           // bit e: what the values of the lane's entry hold
 #pragma unroll
     for (int r = 0; r < R; ++r) zero[r] = 0;               // an infinity without weight in row r
-    for (int j = j0; j < j1 && !__all_sync(0xFFFFFFFFu, nan == kAll); j += 32) {
+    for (unsigned j = j0; j < j1 && !__all_sync(0xFFFFFFFFu, nan == kAll); j += 32) {
       const int64_t mine = place_of(j + lane);
       constexpr int kBatch = 8;
 #pragma unroll 1
@@ -273,7 +274,7 @@ __device__ __noinline__ void mend_sums(const PagedAttnParams& p, const int* pre,
       if (!__any_sync(0xFFFFFFFFu, fix != 0)) continue;
       if (__all_sync(0xFFFFFFFFu, have == kAll)) {         // all of a row: its scores may be the reason
         bool lost = false;
-        for (int j = j0; j < j1 && !__any_sync(0xFFFFFFFFu, lost); j += 32) {
+        for (unsigned j = j0; j < j1 && !__any_sync(0xFFFFFFFFu, lost); j += 32) {
           const int64_t at = place_of(j + lane);
           float s = 0.f;
           for (int e = 0; e < D && at >= 0; e += 8) {
