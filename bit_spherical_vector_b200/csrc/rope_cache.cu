@@ -25,7 +25,7 @@
 // 2.1 us for one row against 1.5.)
 //
 // B200, in a CUDA graph: 2048 rows of 32 + 8 + 8 heads of 128, bf16, 12.9 us =
-// 3.9 TB/s (copy rate 6.6); 777 rows of 14 + 2 + 2 heads of 64 3.2 us, one row 1.5 us.
+// 3.9 TB/s (copy rate 6.6); 777 rows of 14 + 2 + 2 heads of 64 3.2 us, one row 1.5 to 1.7 us.
 // The 2048 rows are bound by latency on too few warps: 71 registers leave 28 warps an
 // SM, so their 8192 warps run in two waves, each through its own chain of slot,
 // position, sines and loads; schedulers issue in 57 % of the cycles, and HBM is at 59 %
